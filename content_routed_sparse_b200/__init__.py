@@ -8,7 +8,8 @@ is missing; there is no fallback.
 
 Functions (same names as the C entry points, without the ``crs_`` prefix):
   lsh_route, lsh_attn, indexer_topk, block_describe, block_select,
-  block_quantize, block_select_fp4, sparse_attn, get_device_error.
+  block_quantize, block_select_fp4, sparse_attn, rope, mass_select,
+  get_device_error; KvCache wraps the paged decode cache (crs_cache_*).
 """
 from __future__ import annotations
 
@@ -34,7 +35,7 @@ CRS_IDX_PREFILL, CRS_IDX_DECODE = 0, 1
 STATUS = {0: "CRS_OK", 1: "CRS_ERR_INVALID_ARG", 2: "CRS_ERR_UNSUPPORTED", 3: "CRS_ERR_CUDA",
           4: "CRS_ERR_NONFINITE", 5: "CRS_ERR_TIMEOUT", 6: "CRS_ERR_WORKSPACE",
           7: "CRS_ERR_INDEX"}
-DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INDEX = 0x1, 0x2, 0x4
+DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INDEX, DEVERR_CAPACITY = 0x1, 0x2, 0x4, 0x8
 
 
 class CrsError(RuntimeError):
@@ -97,6 +98,30 @@ class AttnParams(ctypes.Structure):
     _fields_ = [("n_rows", ctypes.c_int), ("n_q", ctypes.c_int), ("n_kv", ctypes.c_int),
                 ("D", ctypes.c_int), ("max_idx", ctypes.c_int), ("n_lists", ctypes.c_int),
                 ("n_keys", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("D", "rot_begin", "rot_dim", "interleaved", "inverse")] + \
+               [("mscale", ctypes.c_float)]
+
+
+class CacheParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seq", "n_kv", "D", "page_size", "max_pages", "n_pages", "cap")]
+
+
+class CacheState(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pool", "v_pool", "block_table", "pos", "mass", "seq_len",
+                                               "next_pos")]
+
+
+class CacheAttnParams(ctypes.Structure):
+    _fields_ = [("c", CacheParams)] + [(n, ctypes.c_int) for n in ("n_q", "n_tok", "prefix_len", "out_dtype",
+                                                                   "want_mass")] + \
+               [("scale", ctypes.c_float), ("decay", ctypes.c_float)]
+
+
+class MassSelectParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seq", "n_kv", "cap", "keep", "sink_end", "window")]
 
 
 class KernelStat(ctypes.Structure):
@@ -173,6 +198,20 @@ _sig("crs_sparse_attn_workspace_size", _SZ, [ctypes.POINTER(AttnParams)])
 _sig("crs_sparse_attn", ctypes.c_int, [ctypes.POINTER(AttnParams), _VP, _VP, _VP, _VP, _VP, _VP,
                                         _VP, _VP, _VP, _VP, _SZ, _VP])
 
+_I64 = ctypes.c_int64
+_sig("crs_rope", ctypes.c_int, [ctypes.POINTER(RopeParams), ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP, _I64, _VP,
+                                _VP, _VP, _I64, _VP])
+_sig("crs_cache_append", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState),
+                                        ctypes.POINTER(RopeParams), _VP, ctypes.c_int, _VP, _VP, _I64, _VP, _I64, _VP,
+                                        _I64, ctypes.c_int, _VP, _VP])
+_sig("crs_cache_commit", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState), ctypes.c_int, _VP,
+                                        _VP])
+_sig("crs_cache_attn_workspace_size", _SZ, [ctypes.POINTER(CacheAttnParams)])
+_sig("crs_cache_attn", ctypes.c_int, [ctypes.POINTER(CacheAttnParams), ctypes.POINTER(CacheState), _VP, _VP, _VP, _VP,
+                                      _VP, _VP, _VP, _VP, _SZ, _VP])
+_sig("crs_mass_select", ctypes.c_int, [ctypes.POINTER(MassSelectParams), _VP, _VP, _VP, _VP, _VP, _VP, _VP])
+_sig("crs_cache_evict", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState), ctypes.c_int, _VP,
+                                       _VP, _VP])
 
 _sig("crs_profile_set", ctypes.c_int, [ctypes.c_int])
 _sig("crs_profile_collect", ctypes.c_int, [ctypes.POINTER(KernelStat), ctypes.c_int,
@@ -897,3 +936,323 @@ def sparse_attn(Q, K, V, I, kv_base=None, scale=None, key_valid=None, q_pos=None
                               _ptr(ws), wsb, _stream(stream))
     _check("crs_sparse_attn", st)
     return out, lse
+
+
+# ------------------------------------------------------- rotary positions --
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, factor: float = 1.0, scaling: str = "linear",
+                  trained_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Radians per position of each rotated pair, [rot_dim / 2] float64, for rope and
+    KvCache.append.  factor > 1 stretches the positions by that much: "linear" divides
+    every frequency by it; "base" enlarges the base so that the slowest pair is
+    stretched by it and the fastest is unchanged; "parts" divides the pairs that make
+    fewer than beta_slow turns over trained_len positions, leaves those that make more
+    than beta_fast, and blends in between."""
+    if rot_dim < 2 or rot_dim % 2 or base <= 1.0 or factor <= 0.0:
+        raise ValueError("rope_inv_freq: even rot_dim >= 2, base > 1 and factor > 0 expected")
+    if scaling == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    elif scaling not in ("linear", "base", "parts"):
+        raise ValueError(f"rope_inv_freq: unknown scaling {scaling!r}")
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    if scaling == "linear" or (scaling == "base" and rot_dim == 2):
+        f = f / factor
+    elif scaling == "parts":
+        j = torch.arange(rot_dim // 2, dtype=torch.float64)
+
+        def pair_of(turns):        # the pair that makes this many turns over the trained length
+            return rot_dim * math.log(trained_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo, hi = math.floor(pair_of(beta_fast)), math.ceil(pair_of(beta_slow))
+        lo, hi = max(lo, 0), min(hi, rot_dim // 2 - 1)
+        ramp = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - ramp) + f / factor * ramp
+    return f.to(device)
+
+
+def _on_current(t: torch.Tensor, name: str):
+    """The launch goes to the current device: a tensor of another one is refused."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, device):
+    """A tensor whose last two dims are dense and whose leading dims are evenly spaced
+    token rows (a slice of a wider projection, say); returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[-1] * shape[-2]
+    st, sz = t.stride(), t.shape
+    row = step = None
+    for d in range(t.dim() - 3, -1, -1):
+        if sz[d] == 1:
+            continue
+        if row is None:
+            row = step = st[d]
+        elif st[d] != step:
+            row = 0
+        step = step * sz[d]
+    if row is None:
+        row = sz[-1] * sz[-2]
+    if (sz[-1] > 1 and st[-1] != 1) or (sz[-2] > 1 and st[-2] != sz[-1]) or row < sz[-1] * sz[-2]:
+        raise ValueError(f"{name}: dense heads and evenly spaced token rows expected, got strides {st}")
+    return row
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rope(x, pos, inv_freq, *, rot_begin: int = 0, interleaved: bool = False, mscale: float = 1.0,
+         inverse: bool = False, out=None, stream=None):
+    """Rotary positions: x [n_tok, n_heads, D] bf16 or f32 (token rows may be strided), pos
+    [n_tok] int32, inv_freq [rot_dim / 2] float64 -> the rotated x (new, or out; out=x
+    rotates in place).  inverse=True applies the transpose: the gradient of the call."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("rope: x [n_tok, n_heads, D] expected")
+    n_tok, heads, D = x.shape
+    code = _dtype_code(x)
+    _need(pos, "pos", torch.int32, (n_tok,))
+    _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),))
+    _on_current(pos, "pos")
+    _on_current(inv_freq, "inv_freq")
+    xs = _rows(x, "x", x.dtype, x.shape, pos.device)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    ys = _rows(out, "out", x.dtype, x.shape, pos.device)
+    p = RopeParams(D, int(rot_begin), 2 * inv_freq.numel(), int(interleaved), int(inverse), float(mscale))
+    st = _lib.crs_rope(ctypes.byref(p), n_tok, heads, code, x.data_ptr(), xs, pos.data_ptr(), inv_freq.data_ptr(),
+                       out.data_ptr(), ys, _stream(stream))
+    _check("crs_rope", st)
+    return out
+
+
+# ----------------------------------------------------------- decode cache --
+def mass_select(mass, seq_len, keep: int, *, pos=None, next_pos=None, sink_end: int = 0, window: int = 0, idx=None,
+                count=None, stream=None):
+    """The keep slots of each (sequence, KV head) with the most accumulated attention weight:
+    mass [n_seq, n_kv, cap] f32 -> (idx [n_seq, n_kv, keep] int32 ascending, -1 pad; count
+    [n_seq] int32).  With pos [n_seq, n_kv, cap] and next_pos [n_seq] (int32), slots of
+    positions below sink_end and of the last `window` positions are kept first."""
+    _need(mass, "mass", torch.float32)
+    _on_current(mass, "mass")
+    if mass.dim() != 3:
+        raise ValueError("mass_select: mass [n_seq, n_kv, cap] expected")
+    n_seq, n_kv, cap = mass.shape
+    for t, nm, shape in ((seq_len, "seq_len", (n_seq,)), (pos, "pos", (n_seq, n_kv, cap)),
+                         (next_pos, "next_pos", (n_seq,))):
+        if t is not None or nm == "seq_len":
+            _need(t, nm, torch.int32, shape)
+            _on_current(t, nm)
+    if (sink_end > 0 or window > 0) and pos is None:
+        raise ValueError("mass_select: sink_end and window need pos and next_pos")
+    if idx is None:
+        idx = _empty((n_seq, n_kv, keep), torch.int32, mass.device, stream)
+    if count is None:
+        count = _empty((n_seq,), torch.int32, mass.device, stream)
+    _need(idx, "idx", torch.int32, (n_seq, n_kv, keep))
+    _need(count, "count", torch.int32, (n_seq,))
+    p = MassSelectParams(n_seq, n_kv, cap, int(keep), int(sink_end), int(window))
+    st = _lib.crs_mass_select(ctypes.byref(p), _ptr(mass), _ptr(pos), _ptr(seq_len), _ptr(next_pos), _ptr(idx),
+                              _ptr(count), _stream(stream))
+    _check("crs_mass_select", st)
+    return idx, count
+
+
+class KvCache:
+    """Paged K/V cache of a decode batch (crs_cache_* in include/crs.h).  One step:
+
+        q = cache.append(k, v, q=q, inv_freq=f)            # rotate, store behind the cached tokens
+        o, lse = cache.attend(q, prefix_k, prefix_v, mass_out=cache.mass)
+        cache.commit(n_tok)                                # or the accepted drafts of each sequence
+        if due:
+            idx, count = cache.select(keep, window=w)      # heaviest slots of each KV head
+            cache.evict(idx, count)
+
+    The tensors are the caller's: k_pool, v_pool [n_pages, page_size, n_kv, D] bf16,
+    block_table [n_seq, max_pages], seq_len, next_pos [n_seq] int32, pos [n_seq, n_kv, cap]
+    int32 and mass [n_seq, n_kv, cap] f32 (both optional; without them cap is
+    max_pages * page_size).  KvCache.empty allocates them."""
+
+    def __init__(self, k_pool, v_pool, block_table, seq_len, next_pos, pos=None, mass=None):
+        _need(k_pool, "k_pool", torch.bfloat16)
+        if k_pool.dim() != 4:
+            raise ValueError("k_pool must be [n_pages, page_size, n_kv, D]")
+        _need(v_pool, "v_pool", torch.bfloat16, k_pool.shape)
+        n_pages, page_size, n_kv, D = k_pool.shape
+        _need(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [n_seq, max_pages]")
+        n_seq, max_pages = block_table.shape
+        cap = max_pages * page_size
+        for t, nm in ((pos, "pos"), (mass, "mass")):
+            if t is not None:
+                cap = t.shape[-1]
+        _need(seq_len, "seq_len", torch.int32, (n_seq,))
+        _need(next_pos, "next_pos", torch.int32, (n_seq,))
+        if pos is not None:
+            _need(pos, "pos", torch.int32, (n_seq, n_kv, cap))
+        if mass is not None:
+            _need(mass, "mass", torch.float32, (n_seq, n_kv, cap))
+        if cap > max_pages * page_size:
+            raise ValueError(f"pos and mass hold {cap} slots, the block table {max_pages * page_size}")
+        for t in (v_pool, block_table, seq_len, next_pos, pos, mass):
+            if t is not None and t.device != k_pool.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.k_pool, self.v_pool, self.block_table = k_pool, v_pool, block_table
+        self.seq_len, self.next_pos, self.pos, self.mass = seq_len, next_pos, pos, mass
+        self.n_seq, self.n_kv, self.D, self.cap, self.device = n_seq, n_kv, D, cap, k_pool.device
+        self.p = CacheParams(n_seq, n_kv, D, page_size, max_pages, n_pages, cap)
+        self.st = CacheState(*(t.data_ptr() if t is not None else None
+                               for t in (k_pool, v_pool, block_table, pos, mass, seq_len, next_pos)))
+        self._attn_ws = {}
+
+    @classmethod
+    def empty(cls, n_seq, n_kv, max_len, D=128, page_size=64, first_pos=0, track=True, device="cuda"):
+        """A cache of max_len slots per sequence, its pages allocated in order; first_pos is
+        the position of each sequence's first token (the shared prefix's length); track
+        keeps the slots' positions and accumulated weights."""
+        max_pages = -(-max_len // page_size)
+        n_pages = n_seq * max_pages
+        kv = [torch.zeros((n_pages, page_size, n_kv, D), dtype=torch.bfloat16, device=device) for _ in range(2)]
+        table = torch.arange(n_pages, dtype=torch.int32, device=device).view(n_seq, max_pages)
+        ln = torch.zeros((n_seq,), dtype=torch.int32, device=device)
+        nxt = torch.full((n_seq,), int(first_pos), dtype=torch.int32, device=device)
+        pos = torch.zeros((n_seq, n_kv, max_len), dtype=torch.int32, device=device) if track else None
+        mass = torch.zeros((n_seq, n_kv, max_len), dtype=torch.float32, device=device) if track else None
+        return cls(kv[0], kv[1], table, ln, nxt, pos=pos, mass=mass)
+
+    def _counts(self, n_new, name):
+        if n_new is not None:
+            _need(n_new, name, torch.int32, (self.n_seq,))
+            _on_current(n_new, name)
+            return n_new.data_ptr()
+        return None
+
+    def append(self, k, v, q=None, inv_freq=None, n_new=None, *, rot_begin=0, interleaved=False, mscale=1.0,
+               q_out=None, stream=None):
+        """Store k, v [n_seq, n_tok, n_kv, D] behind the cached tokens (token rows may be
+        strided), k rotated by the positions next_pos + i when inv_freq is given; returns q
+        [n_seq, n_tok, n_q, D] rotated likewise (None without q).  n_new [n_seq] int32: how
+        many of each sequence's padded tokens exist.  Lengths advance in commit."""
+        _on_current(self.k_pool, "the cache")
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("append: k [n_seq, n_tok, n_kv, D] expected")
+        n_tok = k.shape[1]
+        shape = (self.n_seq, n_tok, self.n_kv, self.D)
+        ks = _rows(k, "k", torch.bfloat16, shape, self.device)
+        vs = _rows(v, "v", torch.bfloat16, shape, self.device)
+        qs = n_q = 0
+        if q is not None:
+            n_q = q.shape[2]
+            qshape = (self.n_seq, n_tok, n_q, self.D)
+            qs = _rows(q, "q", torch.bfloat16, qshape, self.device)
+            if q_out is None:
+                q_out = _empty(qshape, torch.bfloat16, self.device, stream)
+            _need(q_out, "q_out", torch.bfloat16, qshape)
+        elif q_out is not None:
+            raise ValueError("append: q_out without q")
+        r = fp = None
+        if inv_freq is not None:
+            _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),))
+            _on_current(inv_freq, "inv_freq")
+            r = ctypes.byref(RopeParams(self.D, int(rot_begin), 2 * inv_freq.numel(), int(interleaved), 0,
+                                        float(mscale)))
+            fp = inv_freq.data_ptr()
+        st = _lib.crs_cache_append(ctypes.byref(self.p), ctypes.byref(self.st), r, fp, n_tok,
+                                   self._counts(n_new, "n_new"), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, n_q,
+                                   _ptr(q_out), _stream(stream))
+        _check("crs_cache_append", st)
+        return q_out
+
+    def commit(self, n, n_tok=None, stream=None):
+        """Advance the lengths by n: a number, or accepted tokens per sequence ([n_seq] int32,
+        of at most n_tok appended)."""
+        _on_current(self.k_pool, "the cache")
+        accepted = None
+        if isinstance(n, torch.Tensor):
+            accepted = self._counts(n, "accepted")
+            n = 0x7fffffff if n_tok is None else n_tok
+        st = _lib.crs_cache_commit(ctypes.byref(self.p), ctypes.byref(self.st), int(n), accepted, _stream(stream))
+        _check("crs_cache_commit", st)
+
+    def attend(self, q, prefix_k=None, prefix_v=None, n_new=None, *, scale=None, out_dtype=torch.float32, out=None,
+               lse=None, mass_out=None, decay=1.0, workspace=None, stream=None):
+        """Attention of q [n_seq, n_tok, n_q, D] over the shared prefix [prefix_len, n_kv, D] and
+        each sequence's slots, the appended tokens included (causally) -> (O in out_dtype,
+        f32 or bf16, lse).  mass_out [n_seq, n_kv, cap] f32 (self.mass: in place) receives
+        decay * self.mass plus the weights the slots got."""
+        _on_current(self.k_pool, "the cache")
+        _need(q, "q", torch.bfloat16)
+        if q.dim() != 4 or q.shape[0] != self.n_seq or q.shape[3] != self.D:
+            raise ValueError(f"q must be [{self.n_seq}, n_tok, n_q, {self.D}], got {tuple(q.shape)}")
+        n_tok, n_q = q.shape[1], q.shape[2]
+        plen = 0
+        if (prefix_k is None) != (prefix_v is None):
+            raise ValueError("attend: prefix_k and prefix_v go together")
+        if prefix_k is not None:
+            plen = prefix_k.shape[0]
+            _need(prefix_k, "prefix_k", torch.bfloat16, (plen, self.n_kv, self.D))
+            _need(prefix_v, "prefix_v", torch.bfloat16, (plen, self.n_kv, self.D))
+        if out is None:
+            out = _empty(q.shape, out_dtype, self.device, stream)
+        _need(out, "out", None, q.shape)
+        code = _dtype_code(out)
+        if lse is None:
+            lse = _empty((self.n_seq, n_tok, n_q), torch.float32, self.device, stream)
+        _need(lse, "lse", torch.float32, (self.n_seq, n_tok, n_q))
+        if mass_out is not None:
+            if self.mass is None:
+                raise ValueError("attend: mass_out needs a cache that tracks mass")
+            _need(mass_out, "mass_out", torch.float32, (self.n_seq, self.n_kv, self.cap))
+        for t, nm in ((q, "q"), (prefix_k, "prefix_k"), (prefix_v, "prefix_v"), (out, "out"), (lse, "lse"),
+                      (mass_out, "mass_out"), (workspace, "workspace")):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{nm} must be on {self.device}, got {t.device}")
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.D)
+        p = CacheAttnParams(self.p, n_q, n_tok, plen, code, int(mass_out is not None), float(scale), float(decay))
+        key = (n_q, n_tok, plen, code, mass_out is not None)
+        nbytes = self._attn_ws.get(key)
+        if nbytes is None:
+            nbytes = self._attn_ws[key] = int(_lib.crs_cache_attn_workspace_size(ctypes.byref(p)))
+        if workspace is None:
+            workspace = _empty((max(nbytes, 16),), torch.uint8, self.device, stream)
+        elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous():
+            raise ValueError(f"workspace too small: need {nbytes} contiguous bytes")
+        st = _lib.crs_cache_attn(ctypes.byref(p), ctypes.byref(self.st), q.data_ptr(), self._counts(n_new, "n_new"),
+                                 _ptr(prefix_k) if plen else None, _ptr(prefix_v) if plen else None, out.data_ptr(),
+                                 lse.data_ptr(), _ptr(mass_out), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+        _check("crs_cache_attn", st)
+        return out, lse
+
+    def select(self, keep, *, sink_end=0, window=0, idx=None, count=None, stream=None):
+        """mass_select on this cache's weights, positions and lengths."""
+        if self.mass is None:
+            raise ValueError("select: the cache does not track mass")
+        return mass_select(self.mass, self.seq_len, keep, pos=self.pos,
+                           next_pos=self.next_pos if self.pos is not None else None, sink_end=sink_end,
+                           window=window, idx=idx, count=count, stream=stream)
+
+    def evict(self, idx, count, stream=None):
+        """Keep only the listed slots of each KV head (idx [n_seq, n_kv, keep] ascending, count
+        [n_seq], from select): later ones move into the freed slots, seq_len becomes count."""
+        _on_current(self.k_pool, "the cache")
+        _need(idx, "idx", torch.int32)
+        if idx.dim() != 3 or idx.shape[0] != self.n_seq or idx.shape[1] != self.n_kv:
+            raise ValueError(f"idx must be [{self.n_seq}, {self.n_kv}, keep], got {tuple(idx.shape)}")
+        _on_current(idx, "idx")
+        st = _lib.crs_cache_evict(ctypes.byref(self.p), ctypes.byref(self.st), idx.shape[2], idx.data_ptr(),
+                                  self._counts(count, "count"), _stream(stream))
+        _check("crs_cache_evict", st)

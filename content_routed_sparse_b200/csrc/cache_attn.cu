@@ -1,0 +1,802 @@
+// Decode attention over a prefix shared by the batch and each sequence's own cached
+// slots, with the weights accumulated for eviction, sm_100a.
+//
+// The work is a list of items: (KV head, tile of query rows) over the prefix, where
+// the rows are the whole batch's queries of that head, and (sequence, KV head, tile
+// of its query rows) over its own slots.  An item's keys are cut into tiles of 64.
+// All tiles of all items form one sequence of W tiles, and CTA c of a fixed grid
+// (as many as fit on the GPU) takes tiles [c w, (c + 1) w), w = ceil(W / grid): the
+// lengths live on the device, and ragged batches stay balanced without the host
+// knowing them.  A CTA's share of an item is a piece with its own softmax state
+// (m, l, unnormalised O); piece number = CTA + item, which is unique because one of
+// the two grows from piece to piece.  cache_merge_kernel joins the pieces, divides,
+// and turns the logits kept in the workspace into accumulated weights.
+#include <math.h>
+
+#include "cache.cuh"
+#include "tc.cuh"
+
+namespace crs {
+
+constexpr int kCaKeys = 64;            // keys per tile
+constexpr int kCaWarps = 4;            // each takes 16 keys of a tile
+constexpr int kCaThreads = kCaWarps * 32;
+constexpr int kCaStages = 3;           // K/V tiles in the ring
+constexpr int kCaRows = 16;            // query rows of an item (M of mma.sync)
+constexpr int kCaRing = kCaStages + 1; // tiles whose row lists are kept
+constexpr int kMgThreads = 256;
+constexpr int kMgSlots = 512;          // slots whose mass one CTA updates
+
+struct CaArgs {
+    CacheDev c;
+    const __nv_bfloat16 *Q, *pk, *pv;
+    const int32_t *n_new;
+    int n_q, G, n_tok;
+    int M;             // query rows of one (sequence, KV head): n_tok * G
+    int RT;            // row tiles of an own item
+    int prefix_len;
+    int PT;            // key tiles of a prefix item of cache_attn_kernel (0: none)
+    int PRT;           // its row tiles, over n_seq * M rows
+    int grid;          // CTAs of cache_attn_kernel
+    int tc_splits;     // key splits of cache_prefix_kernel (0: not launched)
+    float scale_log2, decay;
+    float *part_o, *part_ml;       // pieces: [piece][16][D], [piece][16][2] (m in log2 units, l)
+    float *tc_o, *tc_ml;           // [split][KV head][n_seq * M][D], [..][2]
+    float *logits;                 // [sequence][KV head][M][ls] log2-scaled, or null
+    int ls;
+    void *O;
+    float *lse, *mass_out;
+};
+
+// key tiles of a sequence's own items (none without a new token to ask)
+__device__ __forceinline__ int ca_tiles(const CaArgs &a, int s) {
+    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
+    return n > 0 ? (len + n + kCaKeys - 1) / kCaKeys : 0;
+}
+__device__ __forceinline__ long long ca_prefix_tiles(const CaArgs &a) {
+    return (long long)a.c.n_kv * a.PRT * a.PT;
+}
+__device__ __forceinline__ long long ca_share(const CaArgs &a, long long W) {
+    return W > a.grid ? (W + a.grid - 1) / a.grid : 1;
+}
+
+// Position in the tile sequence.
+struct CaCursor {
+    bool prefix;
+    int s, h, rt;      // own: sequence, KV head, row tile; prefix: h, rt
+    int t, T;          // tile of the item, tiles of the item
+};
+
+__device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const int *cum, long long n) {
+    CaCursor u;
+    const long long P = ca_prefix_tiles(a);
+    u.prefix = n < P;
+    if (u.prefix) {
+        const int x = (int)(n / a.PT);
+        u.s = 0;
+        u.h = x / a.PRT;
+        u.rt = x - u.h * a.PRT;
+        u.t = (int)(n - (long long)x * a.PT);
+        u.T = a.PT;
+        return u;
+    }
+    n -= P;
+    const long long K = (long long)a.c.n_kv * a.RT;
+    int lo = 0, hi = a.c.n_seq;                 // cum[lo] K <= n < cum[hi] K
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)cum[mid] * K <= n) lo = mid;
+        else hi = mid;
+    }
+    const long long r = n - (long long)cum[lo] * K;
+    u.s = lo;
+    u.T = cum[lo + 1] - cum[lo];
+    const int y = (int)(r / u.T);
+    u.t = (int)(r - (long long)y * u.T);
+    u.h = y / a.RT;
+    u.rt = y - u.h * a.RT;
+    return u;
+}
+// the next tile; past the last one the cursor must not be used
+__device__ __forceinline__ void ca_advance(const CaArgs &a, const int *cum, CaCursor &u) {
+    if (++u.t < u.T) return;
+    u.t = 0;
+    if (++u.rt < (u.prefix ? a.PRT : a.RT)) return;
+    u.rt = 0;
+    if (++u.h < a.c.n_kv) return;
+    u.h = 0;
+    if (u.prefix) {
+        u.prefix = false;
+        u.s = 0;
+    } else {
+        ++u.s;
+    }
+    while (u.s < a.c.n_seq && cum[u.s + 1] == cum[u.s]) ++u.s;
+    u.T = u.s < a.c.n_seq ? cum[u.s + 1] - cum[u.s] : 1;
+}
+__device__ __forceinline__ long long ca_item(const CaArgs &a, const CaCursor &u) {
+    return u.prefix ? (long long)u.h * a.PRT + u.rt
+                    : (long long)a.c.n_kv * a.PRT + ((long long)u.s * a.c.n_kv + u.h) * a.RT + u.rt;
+}
+
+// cum[s] = tiles of the sequences before s, s = 0..n_seq (one block; barriers inside)
+__device__ __forceinline__ void ca_cumulate(const CaArgs &a, int *cum, int *scratch) {
+    const int n = a.c.n_seq, per = (n + kCaThreads - 1) / kCaThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) {
+        const int T = ca_tiles(a, s);
+        cum[s + 1] = T;
+        sum += T;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += scratch[w];
+    for (int s = s0; s < s1; ++s) {
+        base += cum[s + 1];
+        cum[s + 1] = base;
+    }
+    if (tid == 0) cum[0] = 0;
+    __syncthreads();
+}
+
+// The query row R of an item: its token's index, whether it exists, where it lies.
+struct CaRow {
+    int lim;                       // keys it sees (slots or prefix keys below lim)
+    const __nv_bfloat16 *q;        // null: no such row
+};
+__device__ __forceinline__ CaRow ca_row(const CaArgs &a, const CaCursor &u, int r) {
+    CaRow w;
+    w.lim = 0;
+    w.q = nullptr;
+    int R = u.rt * kCaRows + r, s = u.s;
+    if (u.prefix) {
+        if (R >= a.c.n_seq * a.M) return w;
+        s = R / a.M;
+        R -= s * a.M;
+    } else if (R >= a.M) {
+        return w;
+    }
+    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
+    const int i = R / a.G, g = R - i * a.G;
+    if (i >= n) return w;
+    w.lim = u.prefix ? a.prefix_len : len + i + 1;
+    w.q = a.Q + (((size_t)s * a.n_tok + i) * a.n_q + u.h * a.G + g) * a.c.D;
+    return w;
+}
+
+template <int D> constexpr int ca_tile_bytes() { return kCaKeys * D * 2; }
+template <int D> constexpr int ca_scratch_bytes() { return D / 8 * 32 * 16; }
+template <int D> constexpr int ca_smem_bytes(int n_seq) {
+    return 2 * kCaStages * ca_tile_bytes<D>() + ca_scratch_bytes<D>() + kCaRing * kCaKeys * 4 + kCaRing * 2 * 8 +
+           kCaWarps * 16 * 2 * 4 + 64 + (n_seq + 1) * 4;
+}
+
+// CTAs per SM: as many as the shared memory (108 and 55 KB) and the registers hold
+template <int D> constexpr int ca_per_sm() { return D == 128 ? 2 : 4; }
+
+// byte offset of 16-byte chunk c of row r of a tile (rows of 2 D bytes, chunks XORed by row)
+template <int D> __device__ __forceinline__ int ca_off(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(CaArgs a) {
+    extern __shared__ __align__(128) unsigned char ca_smem[];
+    constexpr int kTile = ca_tile_bytes<D>(), kChunks = D / 8;
+    unsigned char *sK = ca_smem;                                       // [stages][64 rows][2 D bytes]
+    unsigned char *sV = sK + kCaStages * kTile;
+    float4 *sAcc = reinterpret_cast<float4 *>(sV + kCaStages * kTile); // [D / 8][32 lanes]
+    const __nv_bfloat16 **sBase = reinterpret_cast<const __nv_bfloat16 **>(sAcc + D / 8 * 32);   // [ring][K, V]
+    int *sRow = reinterpret_cast<int *>(sBase + kCaRing * 2);          // [ring][64]: token row, -1: none
+    float *sM = reinterpret_cast<float *>(sRow + kCaRing * kCaKeys);   // [warps][16]
+    float *sL = sM + kCaWarps * 16;
+    int *sScan = reinterpret_cast<int *>(sL + kCaWarps * 16);
+    int *cum = sScan + 16;                                             // [n_seq + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g_row = lane >> 2, tig = lane & 3;
+
+    ca_cumulate(a, cum, sScan);
+    const long long W = ca_prefix_tiles(a) + (long long)cum[a.c.n_seq] * a.c.n_kv * a.RT;
+    const long long w = ca_share(a, W);
+    const long long n0 = blockIdx.x * w;
+    if (n0 >= W) return;
+    const int n_tiles = (int)min(w, W - n0);
+
+    const size_t tok_stride = (size_t)a.c.n_kv * D;
+    CaCursor ahead = ca_seek(a, cum, n0);        // next tile whose rows are listed
+    CaCursor cur = ahead;                        // tile being consumed
+
+    // rows of the ahead tile into ring slot i % kCaRing
+    auto list_tile = [&](int i) {
+        if (i >= n_tiles) return;
+        const int slot = i % kCaRing;
+        if (tid < kCaKeys) {
+            const int j = ahead.t * kCaKeys + tid;
+            int row = -1;
+            if (ahead.prefix) {
+                if (j < a.prefix_len) row = j;
+            } else {
+                const int len = cache_len(a.c, ahead.s);
+                if (j < len + cache_new(a.c, a.n_new, a.n_tok, ahead.s, len)) row = cache_row(a.c, ahead.s, j);
+            }
+            sRow[slot * kCaKeys + tid] = row;
+            if (tid == 0) {
+                sBase[slot * 2] = (ahead.prefix ? a.pk : a.c.k) + ahead.h * D;
+                sBase[slot * 2 + 1] = (ahead.prefix ? a.pv : a.c.v) + ahead.h * D;
+            }
+        }
+        ca_advance(a, cum, ahead);
+    };
+    // 16-byte copies of tile i's K and V rows (one commit group, empty past the last tile)
+    auto load_tile = [&](int i) {
+        if (i < n_tiles) {
+            const int slot = i % kCaRing, buf = i % kCaStages;
+            const __nv_bfloat16 *Kb = sBase[slot * 2], *Vb = sBase[slot * 2 + 1];
+#pragma unroll
+            for (int e0 = 0; e0 < kCaKeys * kChunks / kCaThreads; ++e0) {
+                const int e = tid + e0 * kCaThreads;
+                const int r = e / kChunks, c = e % kChunks;
+                const int row = sRow[slot * kCaKeys + r];
+                const bool ok = row >= 0;
+                const size_t off = ok ? (size_t)row * tok_stride + c * 8 : 0;
+                cp_async16_zfill(sK + buf * kTile + ca_off<D>(r, c), Kb + off, ok);
+                cp_async16_zfill(sV + buf * kTile + ca_off<D>(r, c), Vb + off, ok);
+            }
+        }
+        cp_async_commit();
+    };
+
+    for (int i = 0; i < kCaStages; ++i) list_tile(i);
+    __syncthreads();
+    for (int i = 0; i < kCaStages - 1; ++i) load_tile(i);
+
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m_lo, m_hi, l_lo, l_hi;
+    int lim_lo = 0, lim_hi = 0, lim_max = 0;
+    float *log_lo = nullptr, *log_hi = nullptr;
+    bool fresh = true;                           // the next tile starts a piece
+
+    for (int i = 0; i < n_tiles; ++i) {
+        const int buf = i % kCaStages, slot = i % kCaRing;
+        if (fresh) {                             // query fragments straight from global memory
+            fresh = false;
+            const CaRow lo = ca_row(a, cur, g_row), hi = ca_row(a, cur, g_row + 8);
+            lim_lo = lo.lim;
+            lim_hi = hi.lim;
+            lim_max = __reduce_max_sync(0xffffffffu, max(lim_lo, lim_hi));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = kk * 16 + e * 8 + tig * 2;
+                    qf[kk][2 * e] = lo.q ? *reinterpret_cast<const uint32_t *>(lo.q + col) : 0u;
+                    qf[kk][2 * e + 1] = hi.q ? *reinterpret_cast<const uint32_t *>(hi.q + col) : 0u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+            m_lo = m_hi = -INFINITY;
+            l_lo = l_hi = 0.0f;
+            log_lo = log_hi = nullptr;
+            if (a.logits && !cur.prefix) {
+                float *base = a.logits + ((size_t)cur.s * a.c.n_kv + cur.h) * a.M * a.ls;
+                const int R = cur.rt * kCaRows + g_row;
+                if (R < a.M) log_lo = base + (size_t)R * a.ls;
+                if (R + 8 < a.M) log_hi = base + (size_t)(R + 8) * a.ls;
+            }
+        }
+        cp_async_wait<kCaStages - 2>();          // tile i has landed (this thread's copies)
+        __syncthreads();                         // ... everyone's; tile i - 1 is no longer read
+        load_tile(i + kCaStages - 1);            // into the buffer of tile i - 1
+        list_tile(i + kCaStages);                // over the rows of tile i - 1
+        const int kw = warp * 16;                // this warp's 16 keys
+        const int j0 = cur.t * kCaKeys + kw;
+        const int *rows = sRow + slot * kCaKeys + kw;
+        if (j0 < lim_max) {
+            const uint32_t kb = smem_u32(sK + buf * kTile), vb = smem_u32(sV + buf * kTile);
+            float s[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                // (keys 0-7, dims lo), (keys 0-7, dims hi), (keys 8-15, lo), (keys 8-15, hi)
+                const int mi = lane >> 3, r = kw + (lane & 7) + ((mi >> 1) << 3), c = kk * 2 + (mi & 1);
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(kb + ca_off<D>(r, c), b0, b1, b2, b3);
+                mma_bf16(s[0], qf[kk], b0, b1);
+                mma_bf16(s[1], qf[kk], b2, b3);
+            }
+            float mx_lo = -INFINITY, mx_hi = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = nt * 8 + tig * 2 + e;
+                    const bool ok = rows[key] >= 0;
+                    s[nt][e] = ok && j0 + key < lim_lo ? s[nt][e] * a.scale_log2 : -INFINITY;
+                    s[nt][2 + e] = ok && j0 + key < lim_hi ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
+                    mx_lo = fmax_nan(mx_lo, s[nt][e]);
+                    mx_hi = fmax_nan(mx_hi, s[nt][2 + e]);
+                }
+                const int key = nt * 8 + tig * 2;
+                if (log_lo) *reinterpret_cast<float2 *>(log_lo + j0 + key) = make_float2(s[nt][0], s[nt][1]);
+                if (log_hi) *reinterpret_cast<float2 *>(log_hi + j0 + key) = make_float2(s[nt][2], s[nt][3]);
+            }
+            mx_lo = fmax_nan(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 1));
+            mx_lo = fmax_nan(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 2));
+            mx_hi = fmax_nan(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 1));
+            mx_hi = fmax_nan(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 2));
+            const float mn_lo = fmax_nan(m_lo, mx_lo), mn_hi = fmax_nan(m_hi, mx_hi);   // a NaN logit stays one
+            const float c_lo = (mn_lo == -INFINITY) ? 1.0f : sa_ex2(m_lo - mn_lo);
+            const float c_hi = (mn_hi == -INFINITY) ? 1.0f : sa_ex2(m_hi - mn_hi);
+            float ps_lo = 0.0f, ps_hi = 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s[nt][e] = (s[nt][e] == -INFINITY) ? 0.0f : sa_ex2(s[nt][e] - mn_lo);
+                    s[nt][2 + e] = (s[nt][2 + e] == -INFINITY) ? 0.0f : sa_ex2(s[nt][2 + e] - mn_hi);
+                    ps_lo += s[nt][e];
+                    ps_hi += s[nt][2 + e];
+                }
+            }
+            l_lo = l_lo * c_lo + ps_lo;
+            l_hi = l_hi * c_hi + ps_hi;
+            m_lo = mn_lo;
+            m_hi = mn_hi;
+            if (c_lo != 1.0f || c_hi != 1.0f) {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][0] *= c_lo; o[j][1] *= c_lo;
+                    o[j][2] *= c_hi; o[j][3] *= c_hi;
+                }
+            }
+            // f32 output: P = P_hi + P_lo, both bf16 (about 16 significant bits); bf16 output:
+            // P rounded once, half a bf16 step, as the output itself is
+            uint32_t pa[4], pl[4];
+            if constexpr (SPLIT) {
+                pack_bf16_split(s[0][0], s[0][1], pa[0], pl[0]);
+                pack_bf16_split(s[0][2], s[0][3], pa[1], pl[1]);
+                pack_bf16_split(s[1][0], s[1][1], pa[2], pl[2]);
+                pack_bf16_split(s[1][2], s[1][3], pa[3], pl[3]);
+            } else {
+                pa[0] = pack_bf16(s[0][0], s[0][1]);
+                pa[1] = pack_bf16(s[0][2], s[0][3]);
+                pa[2] = pack_bf16(s[1][0], s[1][1]);
+                pa[3] = pack_bf16(s[1][2], s[1][3]);
+            }
+#pragma unroll
+            for (int jj = 0; jj < D / 16; ++jj) {
+                // (keys 0-7, dims 16jj..), (keys 8-15, dims 16jj..), (keys 0-7, 16jj+8..), (keys 8-15, 16jj+8..)
+                const int mi = lane >> 3, r = kw + (lane & 7) + ((mi & 1) << 3), c = jj * 2 + (mi >> 1);
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4_t(vb + ca_off<D>(r, c), b0, b1, b2, b3);
+                mma_bf16(o[2 * jj], pa, b0, b1);
+                mma_bf16(o[2 * jj + 1], pa, b2, b3);
+                if constexpr (SPLIT) {
+                    mma_bf16(o[2 * jj], pl, b0, b1);
+                    mma_bf16(o[2 * jj + 1], pl, b2, b3);
+                }
+            }
+        } else if (a.logits && !cur.prefix) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const int key = nt * 8 + tig * 2;
+                if (log_lo) *reinterpret_cast<float2 *>(log_lo + j0 + key) = make_float2(-INFINITY, -INFINITY);
+                if (log_hi) *reinterpret_cast<float2 *>(log_hi + j0 + key) = make_float2(-INFINITY, -INFINITY);
+            }
+        }
+
+        // ---- end of the piece: the warps' states are joined in warp order through 16 D floats
+        if (cur.t == cur.T - 1 || i == n_tiles - 1) {
+            fresh = true;
+            l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
+            l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
+            l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
+            l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
+            if (tig == 0) {
+                sM[warp * 16 + g_row] = m_lo;
+                sM[warp * 16 + g_row + 8] = m_hi;
+                sL[warp * 16 + g_row] = l_lo;
+                sL[warp * 16 + g_row + 8] = l_hi;
+            }
+            __syncthreads();
+            float M_lo = -INFINITY, M_hi = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < kCaWarps; ++v) {
+                M_lo = fmax_nan(M_lo, sM[v * 16 + g_row]);
+                M_hi = fmax_nan(M_hi, sM[v * 16 + g_row + 8]);
+            }
+            const float f_lo = m_lo == -INFINITY ? 0.0f : sa_ex2(m_lo - M_lo);
+            const float f_hi = m_hi == -INFINITY ? 0.0f : sa_ex2(m_hi - M_hi);
+#pragma unroll
+            for (int v = kCaWarps - 1; v >= 0; --v) {
+                if (warp == v) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        float4 x = make_float4(o[j][0] * f_lo, o[j][1] * f_lo, o[j][2] * f_hi, o[j][3] * f_hi);
+                        if (v < kCaWarps - 1) {
+                            const float4 y = sAcc[j * 32 + lane];
+                            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                        }
+                        if (v > 0) {
+                            sAcc[j * 32 + lane] = x;
+                        } else {
+                            o[j][0] = x.x; o[j][1] = x.y; o[j][2] = x.z; o[j][3] = x.w;
+                        }
+                    }
+                }
+                if (v > 0) __syncthreads();
+            }
+            if (warp == 0) {
+                const size_t piece = (size_t)(blockIdx.x + ca_item(a, cur));
+                float *po = a.part_o + piece * (kCaRows * D);
+                float *pm = a.part_ml + piece * (kCaRows * 2);
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    const int col = j * 8 + tig * 2;
+                    if (lim_lo > 0) *reinterpret_cast<float2 *>(po + g_row * D + col) = make_float2(o[j][0], o[j][1]);
+                    if (lim_hi > 0)
+                        *reinterpret_cast<float2 *>(po + (g_row + 8) * D + col) = make_float2(o[j][2], o[j][3]);
+                }
+                if (lane < kCaRows) {
+                    float Mx = -INFINITY, L = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < kCaWarps; ++v) Mx = fmax_nan(Mx, sM[v * 16 + lane]);
+#pragma unroll
+                    for (int v = 0; v < kCaWarps; ++v)
+                        if (sM[v * 16 + lane] != -INFINITY) L += sL[v * 16 + lane] * sa_ex2(sM[v * 16 + lane] - Mx);
+                    *reinterpret_cast<float2 *>(pm + lane * 2) = make_float2(Mx, L);
+                }
+            }
+            __syncthreads();                     // sM, sL and sAcc are reused
+        }
+        ca_advance(a, cum, cur);
+    }
+    cp_async_wait<0>();
+}
+
+// --------------------------------------------------------------------------- merge --
+// A row's pieces: first those of its own item, then the prefix's.
+struct MgRow {
+    long long own0, pre0;      // first piece number
+    int n_own, n_pre;
+    int r_own, r_pre;          // row within the pieces' 16
+    int h;
+    long long r_tc;            // row of the tensor-core prefix pass
+};
+__device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, int before, int T, long long W) {
+    MgRow m;
+    const long long w = ca_share(a, W), P = ca_prefix_tiles(a);
+    m.n_own = m.n_pre = 0;
+    m.own0 = m.pre0 = 0;
+    m.h = h;
+    const int rt = R / kCaRows;
+    m.r_own = R - rt * kCaRows;
+    if (T > 0) {
+        const long long x = ((long long)s * a.c.n_kv + h) * a.RT + rt;
+        const long long first = P + (long long)before * a.c.n_kv * a.RT + ((long long)h * a.RT + rt) * T;
+        const long long c0 = first / w, c1 = (first + T - 1) / w;
+        m.own0 = c0 + (long long)a.c.n_kv * a.PRT + x;
+        m.n_own = (int)(c1 - c0 + 1);
+    }
+    const long long Rg = (long long)s * a.M + R;
+    m.r_tc = Rg;
+    if (a.PT > 0) {
+        const int prt = (int)(Rg / kCaRows);
+        m.r_pre = (int)(Rg - (long long)prt * kCaRows);
+        const long long x = (long long)h * a.PRT + prt, first = x * a.PT;
+        const long long c0 = first / w, c1 = (first + a.PT - 1) / w;
+        m.pre0 = c0 + x;
+        m.n_pre = (int)(c1 - c0 + 1);
+    } else {
+        m.r_pre = 0;
+        m.n_pre = a.tc_splits;
+    }
+    return m;
+}
+// index of piece p of the row: its (m, l) pair and its D floats, in the arrays ml and o
+__device__ __forceinline__ size_t mg_piece(const CaArgs &a, const MgRow &m, int p, const float *&o, const float *&ml) {
+    o = a.part_o;
+    ml = a.part_ml;
+    if (p < m.n_own) return (size_t)(m.own0 + p) * kCaRows + m.r_own;
+    if (a.PT > 0) return (size_t)(m.pre0 + p - m.n_own) * kCaRows + m.r_pre;
+    o = a.tc_o;
+    ml = a.tc_ml;
+    return ((size_t)(p - m.n_own) * a.c.n_kv + m.h) * ((size_t)a.c.n_seq * a.M) + (size_t)m.r_tc;
+}
+
+// largest m and total l of the row's pieces (one warp; -inf and 0 when there is nothing)
+__device__ __forceinline__ void mg_stat(const CaArgs &a, const MgRow &m, int lane, float &Mx, float &L) {
+    const int n = m.n_own + m.n_pre;
+    const float *o, *ml;
+    float mx = -INFINITY;
+    for (int p = lane; p < n; p += 32) {
+        const size_t k = mg_piece(a, m, p, o, ml);
+        mx = fmaxf(mx, ml[k * 2]);
+    }
+    Mx = warp_max(mx);
+    float l = 0.0f;
+    for (int p = lane; p < n; p += 32) {
+        const size_t k = mg_piece(a, m, p, o, ml);
+        const float2 v = *reinterpret_cast<const float2 *>(ml + k * 2);
+        if (v.x != -INFINITY) l += v.y * exp2f(v.x - Mx);
+    }
+    L = warp_sum(l);
+}
+
+// tiles of the sequences before s, and of all (one block)
+__device__ __forceinline__ void mg_before(const CaArgs &a, int s, int &before, int &all) {
+    __shared__ int red[2][kMgThreads / 32];
+    int b = 0, t = 0;
+    for (int q = threadIdx.x; q < a.c.n_seq; q += kMgThreads) {
+        const int T = ca_tiles(a, q);
+        t += T;
+        if (q < s) b += T;
+    }
+    b = warp_sum_int(b);
+    t = warp_sum_int(t);
+    if ((threadIdx.x & 31) == 0) {
+        red[0][threadIdx.x >> 5] = b;
+        red[1][threadIdx.x >> 5] = t;
+    }
+    __syncthreads();
+    before = all = 0;
+#pragma unroll
+    for (int v = 0; v < kMgThreads / 32; ++v) {
+        before += red[0][v];
+        all += red[1][v];
+    }
+}
+
+// CTAs [0, n_o) join pieces: WPR warps per row, 8 / WPR rows of one (sequence, KV head)
+// each; the CTAs after them update kMgSlots slots' mass each.
+template <int D, int WPR, typename OutT>
+__global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int n_o, int row_groups, int chunks) {
+    constexpr int kRowsPer = 8 / WPR, kE = D / 32;
+    extern __shared__ float mg_smem[];           // mass CTAs: [M] lse in log2 units
+    __shared__ float red[8][D];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool joins = (int)blockIdx.x < n_o;
+    const int idx = joins ? blockIdx.x : blockIdx.x - n_o;
+    const int per = joins ? row_groups : chunks;
+    const int sh = idx / per, part = idx - sh * per;
+    const int s = sh / a.c.n_kv, h = sh - s * a.c.n_kv;
+    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
+    const int total = len + n;
+    if (!joins && part * kMgSlots >= total) return;
+    int before, all;
+    mg_before(a, s, before, all);
+    const long long W = ca_prefix_tiles(a) + (long long)all * a.c.n_kv * a.RT;
+    const int T = n > 0 ? (total + kCaKeys - 1) / kCaKeys : 0;
+
+    if (joins) {
+        const int R = part * kRowsPer + warp / WPR, sub = warp % WPR;
+        const int i = R / a.G;
+        const bool exists = R < a.M;
+        const bool live = exists && i < n;
+        float acc[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+        float Mx = -INFINITY, L = 0.0f;
+        if (live) {
+            const MgRow m = mg_row(a, s, h, R, before, T, W);
+            mg_stat(a, m, lane, Mx, L);
+            const int np = m.n_own + m.n_pre;
+            if (Mx != -INFINITY) {
+#pragma unroll 4
+                for (int p = sub; p < np; p += WPR) {
+                    const float *o, *ml;
+                    const size_t k = mg_piece(a, m, p, o, ml);
+                    const float pm = ml[k * 2];
+                    if (pm == -INFINITY) continue;
+                    const float f = exp2f(pm - Mx);
+                    const float *src = o + k * D + lane * kE;
+                    if constexpr (kE == 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(src);
+                        acc[0] += f * v.x; acc[1] += f * v.y; acc[2] += f * v.z; acc[3] += f * v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2 *>(src);
+                        acc[0] += f * v.x; acc[1] += f * v.y;
+                    }
+                }
+            }
+        }
+        if constexpr (WPR > 1) {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
+            __syncthreads();
+            if (sub == 0) {
+#pragma unroll
+                for (int v = 1; v < WPR; ++v)
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) acc[e] += red[warp + v][lane * kE + e];
+            }
+        }
+        if (exists && sub == 0) {
+            const int g = R - i * a.G;
+            const size_t row = ((size_t)s * a.n_tok + i) * a.n_q + h * a.G + g;
+            OutT *dst = static_cast<OutT *>(a.O) + row * D + lane * kE;
+            const float f = L == 0.0f ? 0.0f : 1.0f / L;
+            // nothing seen: zeros; a NaN or infinite sum passes through
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+                const float x = L == 0.0f ? 0.0f : acc[e] * f, y = L == 0.0f ? 0.0f : acc[e + 1] * f;
+                if constexpr (sizeof(OutT) == 4) *reinterpret_cast<float2 *>(dst + e) = make_float2(x, y);
+                else *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(x, y);
+            }
+            if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (Mx + log2f(L)) * 0.6931471805599453f;
+        }
+        return;
+    }
+
+    // ---- mass: sum over the rows of 2^(logit - lse)
+    for (int R = warp; R < a.M; R += 8) {
+        float v = INFINITY;                      // a row that does not exist or sees nothing adds 0
+        if (R / a.G < n) {
+            const MgRow m = mg_row(a, s, h, R, before, T, W);
+            float Mx, L;
+            mg_stat(a, m, lane, Mx, L);
+            if (L != 0.0f) v = Mx + log2f(L);
+        }
+        if (lane == 0) mg_smem[R] = v;
+    }
+    __syncthreads();
+    const float *lg = a.logits + (size_t)sh * a.M * a.ls;
+    const int j = part * kMgSlots + tid * 2;
+    if (j >= total) return;
+    float x = 0.0f, y = 0.0f;
+    const int rows = n * a.G;
+#pragma unroll 4
+    for (int R = 0; R < rows; ++R) {
+        const float2 v = *reinterpret_cast<const float2 *>(lg + (size_t)R * a.ls + j);
+        const float z = mg_smem[R];
+        x += exp2f(v.x - z);
+        y += exp2f(v.y - z);
+    }
+    const size_t at = (size_t)sh * a.c.cap + j;
+    a.mass_out[at] = a.decay * a.c.mass[at] + x;
+    if (j + 1 < total) a.mass_out[at + 1] = a.decay * a.c.mass[at + 1] + y;
+}
+
+// ----------------------------------------------------------------------------- host --
+struct CaPlan {
+    int grid, PT, PRT, RT, M, tc_splits;
+    size_t part_o, part_ml, tc_o, tc_ml, logits, total;   // workspace offsets
+    int ls;
+};
+
+static int ca_validate(const crs_cache_attn_params *p) {
+    if (!p) return CRS_ERR_INVALID_ARG;
+    const int st = cache_validate(&p->c);
+    if (st) return st;
+    if (p->n_q < 1 || p->n_tok < 1 || p->prefix_len < 0) return CRS_ERR_INVALID_ARG;
+    if (p->out_dtype != CRS_F32 && p->out_dtype != CRS_BF16) return CRS_ERR_INVALID_ARG;
+    if (p->n_q % p->c.n_kv != 0 || p->n_q / p->c.n_kv > 64) return CRS_ERR_UNSUPPORTED;
+    if ((long long)p->n_tok * (p->n_q / p->c.n_kv) > 1024) return CRS_ERR_UNSUPPORTED;
+    if (p->prefix_len > 0x7fffffff - 1024 || p->c.cap > 0x7fffffff - 1024) return CRS_ERR_UNSUPPORTED;
+    if ((long long)p->c.n_seq * p->n_tok * p->n_q > 0x3fffffffLL) return CRS_ERR_UNSUPPORTED;
+    return CRS_OK;
+}
+
+static CaPlan ca_plan(const crs_cache_attn_params *p) {
+    CaPlan q;
+    const int G = p->n_q / p->c.n_kv, D = p->c.D;
+    q.M = p->n_tok * G;
+    q.RT = ceil_div(q.M, kCaRows);
+    q.grid = cache_sms() * (D == 128 ? ca_per_sm<128>() : ca_per_sm<64>());
+    q.tc_splits = 0;
+    q.PT = ceil_div(p->prefix_len, kCaKeys);
+    q.PRT = q.PT > 0 ? ceil_div(p->c.n_seq * q.M, kCaRows) : 0;
+    const size_t items = (size_t)p->c.n_kv * q.PRT + (size_t)p->c.n_seq * p->c.n_kv * q.RT;
+    const size_t pieces = items + q.grid;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    size_t at = 0;
+    q.part_o = at;
+    at += up(pieces * kCaRows * D * 4);
+    q.part_ml = at;
+    at += up(pieces * kCaRows * 2 * 4);
+    const size_t tc = (size_t)q.tc_splits * p->c.n_kv * p->c.n_seq * q.M;
+    q.tc_o = at;
+    at += up(tc * D * 4);
+    q.tc_ml = at;
+    at += up(tc * 2 * 4);
+    q.ls = ceil_div(p->c.cap, kCaKeys) * kCaKeys;
+    q.logits = at;
+    if (p->want_mass) at += up((size_t)p->c.n_seq * p->c.n_kv * q.M * q.ls * 4);
+    q.total = at;
+    return q;
+}
+
+template <int D, bool SPLIT> int ca_launch(const CaArgs &a, cudaStream_t s) {
+    const int smem = ca_smem_bytes<D>(a.c.n_seq);
+    CRS_TRY_CUDA(
+        cudaFuncSetAttribute(cache_attn_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    ProfScope _ps(K_CACHE_ATTN, s);
+    cache_attn_kernel<D, SPLIT><<<a.grid, kCaThreads, smem, s>>>(a);
+    CRS_CHECK_LAUNCH();
+    return CRS_OK;
+}
+
+template <int D, typename OutT> int mg_launch(const CaArgs &a, int want_mass, cudaStream_t s) {
+    const long long rows = (long long)a.c.n_seq * a.c.n_kv * a.M;
+    // one warp per row when the rows fill the GPU, else eight share a row's pieces
+    const bool wide = rows < (long long)cache_sms() * 16;
+    const int groups = wide ? a.M : ceil_div(a.M, 8);
+    const long long n_o = (long long)a.c.n_seq * a.c.n_kv * groups;
+    const int chunks = want_mass ? ceil_div(a.c.cap, kMgSlots) : 0;
+    const long long ctas = n_o + (long long)a.c.n_seq * a.c.n_kv * chunks;
+    if (ctas > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
+    ProfScope _ps(K_CACHE_MERGE, s);
+    if (wide) cache_merge_kernel<D, 8, OutT><<<(unsigned)ctas, kMgThreads, a.M * 4, s>>>(a, (int)n_o, groups, chunks);
+    else cache_merge_kernel<D, 1, OutT><<<(unsigned)ctas, kMgThreads, a.M * 4, s>>>(a, (int)n_o, groups, chunks);
+    CRS_CHECK_LAUNCH();
+    return CRS_OK;
+}
+
+}  // namespace crs
+
+using namespace crs;
+
+extern "C" size_t crs_cache_attn_workspace_size(const crs_cache_attn_params *p) {
+    if (ca_validate(p)) return 0;
+    return ca_plan(p).total;
+}
+
+extern "C" int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_state *st, const void *Q,
+                              const int32_t *n_new, const void *prefix_k, const void *prefix_v, void *O, float *lse,
+                              float *mass_out, void *ws, size_t ws_bytes, void *stream) {
+    int e = ca_validate(p);
+    if (e) return e;
+    if ((e = cache_check_state(st))) return e;
+    if (!Q || !O || (p->prefix_len > 0 && (!prefix_k || !prefix_v))) return CRS_ERR_INVALID_ARG;
+    if (p->want_mass && (!mass_out || !st->mass)) return CRS_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(prefix_k) |
+         reinterpret_cast<uintptr_t>(prefix_v) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(ws)) & 15)
+        return CRS_ERR_INVALID_ARG;
+    const CaPlan q = ca_plan(p);
+    if (!ws || ws_bytes < q.total) return CRS_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned char *w = static_cast<unsigned char *>(ws);
+    CaArgs a;
+    a.c = cache_dev(&p->c, st);
+    a.Q = static_cast<const __nv_bfloat16 *>(Q);
+    a.pk = static_cast<const __nv_bfloat16 *>(prefix_k);
+    a.pv = static_cast<const __nv_bfloat16 *>(prefix_v);
+    a.n_new = n_new;
+    a.n_q = p->n_q;
+    a.G = p->n_q / p->c.n_kv;
+    a.n_tok = p->n_tok;
+    a.M = q.M;
+    a.RT = q.RT;
+    a.prefix_len = p->prefix_len;
+    a.PT = q.PT;
+    a.PRT = q.PRT;
+    a.grid = q.grid;
+    a.tc_splits = q.tc_splits;
+    a.scale_log2 = p->scale * kLog2e;
+    a.decay = p->decay;
+    a.part_o = reinterpret_cast<float *>(w + q.part_o);
+    a.part_ml = reinterpret_cast<float *>(w + q.part_ml);
+    a.tc_o = reinterpret_cast<float *>(w + q.tc_o);
+    a.tc_ml = reinterpret_cast<float *>(w + q.tc_ml);
+    a.logits = p->want_mass ? reinterpret_cast<float *>(w + q.logits) : nullptr;
+    a.ls = q.ls;
+    a.O = O;
+    a.lse = lse;
+    a.mass_out = mass_out;
+    const bool f32 = p->out_dtype == CRS_F32;
+    if (p->c.D == 128) e = f32 ? ca_launch<128, true>(a, s) : ca_launch<128, false>(a, s);
+    else e = f32 ? ca_launch<64, true>(a, s) : ca_launch<64, false>(a, s);
+    if (e) return e;
+    if (p->c.D == 128) return f32 ? mg_launch<128, float>(a, p->want_mass, s) : mg_launch<128, __nv_bfloat16>(a, p->want_mass, s);
+    return f32 ? mg_launch<64, float>(a, p->want_mass, s) : mg_launch<64, __nv_bfloat16>(a, p->want_mass, s);
+}

@@ -1,0 +1,294 @@
+// Selection of the slots to keep by accumulated attention weight, and the eviction of
+// the others from the paged cache, sm_100a.
+//
+// Selection: one CTA per (sequence, KV head) holds the slots' order-preserving 32-bit
+// keys in registers, consecutive slots per thread.  The keep-th largest key is found
+// bit by bit from the top, one CTA-wide count per bit, without atomics; a scan of the
+// counts above and at it places the kept slots in ascending order, ties to the lower
+// slot.  Longer caches than the registers hold re-read the keys from memory: four
+// passes with 256-bin histograms, then the same placement.
+//
+// Eviction: nothing depends on the order of a head's slots, so only the kept slots
+// past the new length move, each into a free slot below it: the r-th of the former
+// into the r-th of the latter.  Both are found by binary search in the ascending list
+// (the free slots before entry i number idx[i] - i), so every warp finds its own
+// moves; sources and destinations are disjoint, and the moves run in any order.
+#include "cache.cuh"
+
+namespace crs {
+
+struct MassSelArgs {
+    const float *mass;
+    const int32_t *pos, *seq_len, *next_pos;
+    int32_t *idx, *count;
+    int n_kv, cap, keep, sink_end, window;
+};
+
+__device__ __forceinline__ uint32_t sel_key(float m, int pos, bool has_pos, int sink_end, int recent, bool &nan) {
+    if (has_pos && (pos < sink_end || pos >= recent)) return 0xffffffffu;
+    nan |= m != m;
+    return score_key(m);
+}
+
+// exclusive scan over the CTA of one value per thread (blockDim.x a multiple of 32, one barrier)
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+    uint32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    uint32_t w = lane < n_warps ? warp_sums[lane] : 0u;
+    uint32_t winc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, winc, o);
+        if (lane >= o) winc += u;
+    }
+    total = __shfl_sync(0xffffffffu, winc, 31);
+    return inc - v + __shfl_sync(0xffffffffu, winc - w, warp);
+}
+
+template <int THREADS, int KPT>
+__global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
+    __shared__ uint32_t sums[32];
+    const int sh = blockIdx.x, s = sh / a.n_kv, h = sh - s * a.n_kv;
+    const int tid = threadIdx.x;
+    const int len = min(max(a.seq_len[s], 0), a.cap), k = min(a.keep, len);
+    int32_t *out = a.idx + (size_t)sh * a.keep;
+    if (h == 0 && tid == 0) a.count[s] = k;
+    for (int i = k + tid; i < a.keep; i += THREADS) out[i] = -1;
+    if (len <= a.keep) {
+        for (int i = tid; i < len; i += THREADS) out[i] = i;
+        return;
+    }
+    const float *mass = a.mass + (size_t)sh * a.cap;
+    const int32_t *pos = a.pos ? a.pos + (size_t)sh * a.cap : nullptr;
+    const int recent = a.pos ? a.next_pos[s] - a.window : 0;
+    const int j0 = tid * KPT;
+    uint32_t key[KPT];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        const int j = j0 + i;
+        key[i] = j < len ? sel_key(mass[j], pos ? pos[j] : 0, pos != nullptr, a.sink_end, recent, nan) : 0u;
+    }
+    if (nan) raise_error(CRS_DEVERR_NONFINITE);
+    // the largest threshold that at least k keys reach
+    uint32_t T = 0u;
+    int ph = 0;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t cand = T | (1u << b);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) n += key[i] >= cand;
+        if (cta_count(n, ph) >= k) T = cand;
+    }
+    // slots past len have key 0 and follow every slot of the sequence: they lose every tie
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        gt += key[i] > T;
+        eq += key[i] == T;
+    }
+    uint32_t total;
+    const uint32_t before = cta_scan(gt | (eq << 16), sums, total);
+    const uint32_t need = (uint32_t)k - (total & 0xffffu);
+    uint32_t eb = before >> 16;
+    uint32_t at = (before & 0xffffu) + min(eb, need);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        bool take = key[i] > T;
+        if (key[i] == T) take = eb++ < need;
+        if (take) out[at++] = j0 + i;
+    }
+}
+
+// Any length: the keys stay in memory.
+constexpr int kMassThreads = 1024;
+__global__ void __launch_bounds__(kMassThreads) mass_select_long_kernel(MassSelArgs a) {
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t sums[32];
+    __shared__ uint32_t pick[2];
+    const int sh = blockIdx.x, s = sh / a.n_kv, h = sh - s * a.n_kv;
+    const int tid = threadIdx.x;
+    const int len = min(max(a.seq_len[s], 0), a.cap), k = min(a.keep, len);
+    int32_t *out = a.idx + (size_t)sh * a.keep;
+    if (h == 0 && tid == 0) a.count[s] = k;
+    for (int i = k + tid; i < a.keep; i += kMassThreads) out[i] = -1;
+    if (len <= a.keep) {
+        for (int i = tid; i < len; i += kMassThreads) out[i] = i;
+        return;
+    }
+    const float *mass = a.mass + (size_t)sh * a.cap;
+    const int32_t *pos = a.pos ? a.pos + (size_t)sh * a.cap : nullptr;
+    const int recent = a.pos ? a.next_pos[s] - a.window : 0;
+    bool nan = false;
+    auto key_of = [&](int j) {
+        return sel_key(mass[j], pos ? pos[j] : 0, pos != nullptr, a.sink_end, recent, nan);
+    };
+    // byte by byte from the top: the bin that holds the k-th largest key
+    uint32_t T = 0u, left = (uint32_t)k;
+    for (int b = 24; b >= 0; b -= 8) {
+        if (tid < 256) hist[tid] = 0u;
+        __syncthreads();
+        for (int j = tid; j < len; j += kMassThreads) {
+            const uint32_t key = key_of(j);
+            if (b == 24 || (key >> (b + 8)) == (T >> (b + 8))) {
+                // the keys of a warp mostly share a bin: one addition per group of equal bins
+                const uint32_t bin = (key >> b) & 255u;
+                const unsigned grp = __match_any_sync(__activemask(), bin);
+                if ((int)(tid & 31) == __ffs(grp) - 1) atomicAdd(&hist[bin], (uint32_t)__popc(grp));
+            }
+        }
+        __syncthreads();
+        const uint32_t own = tid < 256 ? hist[255 - tid] : 0u;       // bins from the top
+        uint32_t total;
+        const uint32_t above = cta_scan(own, sums, total);
+        if (tid < 256 && above < left && left <= above + own) {
+            pick[0] = 255u - tid;
+            pick[1] = left - above;
+        }
+        __syncthreads();
+        T |= pick[0] << b;
+        left = pick[1];
+        __syncthreads();
+    }
+    if (nan) raise_error(CRS_DEVERR_NONFINITE);
+    // left = how many of the keys equal to T are kept; slots in order, 1024 at a time
+    uint32_t kept = 0, ties = 0;
+    for (int j0 = 0; j0 < len; j0 += kMassThreads) {
+        const int j = j0 + tid;
+        const uint32_t key = j < len ? key_of(j) : 0u;
+        const uint32_t gt = j < len && key > T, eq = j < len && key == T;
+        uint32_t total;
+        const uint32_t before = cta_scan(gt | (eq << 16), sums, total);
+        const uint32_t eb = ties + (before >> 16);
+        const uint32_t at = kept + (before & 0xffffu) + min(eb, left);
+        if (gt || (eq && eb < left)) out[at] = j;
+        kept += total & 0xffffu;
+        ties += total >> 16;
+        __syncthreads();                         // sums is reused
+    }
+}
+
+// --------------------------------------------------------------------------- evict --
+constexpr int kEvWarps = 8;
+constexpr int kEvBatch = 8;                      // row copies a warp keeps in flight
+
+template <int D>
+__global__ void __launch_bounds__(kEvWarps * 32)
+cache_evict_kernel(CacheDev c, int keep, const int32_t *__restrict__ idx, const int32_t *__restrict__ count) {
+    constexpr int kLanes = D / 4;                // lanes per move: D / 8 for K, D / 8 for V
+    constexpr int kPer = 32 / kLanes;            // moves per warp access
+    const int sh = blockIdx.y, s = sh / c.n_kv, h = sh - s * c.n_kv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = min(max(count[s], 0), min(keep, c.cap));
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) c.seq_len[s] = n;
+    const int32_t *list = idx + (size_t)sh * keep;
+    int lo = 0, hi = n;                          // entries below n
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] < n) lo = mid + 1;
+        else hi = mid;
+    }
+    const int stay = lo, moves = n - stay;
+    const int r = (blockIdx.x * kEvWarps + warp) * 32 + lane;
+    if (r - lane >= moves) return;               // whole warps
+    int src = -1, dst = -1;
+    if (r < moves) {
+        const int from = list[stay + r];
+        int b = 0, e = stay;                     // the first kept slot with more than r free ones before it
+        while (b < e) {
+            const int mid = (b + e) >> 1;
+            if (list[mid] - mid > r) e = mid;
+            else b = mid + 1;
+        }
+        const int to = r + b;
+        if (from >= 0 && from < c.cap) {
+            src = cache_row(c, s, from);
+            dst = cache_row(c, s, to);
+            if (src >= 0 && dst >= 0) {
+                const size_t base = (size_t)sh * c.cap;
+                if (c.pos) c.pos[base + to] = c.pos[base + from];
+                if (c.mass) c.mass[base + to] = c.mass[base + from];
+            }
+        } else {
+            raise_error(CRS_DEVERR_INDEX);
+        }
+    }
+    const int which = lane / kLanes, part = lane % kLanes;
+    __nv_bfloat16 *pool = (part < D / 8 ? c.k : c.v) + (size_t)h * D + (part % (D / 8)) * 8;
+    const size_t stride = (size_t)c.n_kv * D;
+#pragma unroll
+    for (int b = 0; b < 32; b += kEvBatch * kPer) {
+        uint4 v[kEvBatch];
+        int to[kEvBatch];
+#pragma unroll
+        for (int q = 0; q < kEvBatch; ++q) {
+            const int m = b + q * kPer + which;
+            const int from = __shfl_sync(0xffffffffu, src, m);
+            to[q] = __shfl_sync(0xffffffffu, dst, m);
+            if (from < 0) to[q] = -1;
+            if (to[q] >= 0) v[q] = *reinterpret_cast<const uint4 *>(pool + (size_t)from * stride);
+        }
+#pragma unroll
+        for (int q = 0; q < kEvBatch; ++q)
+            if (to[q] >= 0) *reinterpret_cast<uint4 *>(pool + (size_t)to[q] * stride) = v[q];
+    }
+}
+
+}  // namespace crs
+
+using namespace crs;
+
+extern "C" int crs_mass_select(const crs_mass_select_params *p, const float *mass, const int32_t *pos,
+                               const int32_t *seq_len, const int32_t *next_pos, int32_t *idx, int32_t *count,
+                               void *stream) {
+    if (!p || p->n_seq < 1 || p->n_kv < 1 || p->cap < 1 || p->keep < 1 || p->keep > p->cap || p->window < 0)
+        return CRS_ERR_INVALID_ARG;
+    const long long ctas = (long long)p->n_seq * p->n_kv;
+    if (ctas > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
+    if (!mass || !seq_len || !idx || !count || (pos && !next_pos)) return CRS_ERR_INVALID_ARG;
+    MassSelArgs a{mass, pos, seq_len, next_pos, idx, count, p->n_kv, p->cap, p->keep, p->sink_end, p->window};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)ctas;
+    {
+        ProfScope _ps(K_MASS_SELECT, s);
+        if (p->cap <= 1024) mass_select_kernel<256, 4><<<grid, 256, 0, s>>>(a);
+        else if (p->cap <= 2048) mass_select_kernel<256, 8><<<grid, 256, 0, s>>>(a);
+        else if (p->cap <= 4096) mass_select_kernel<512, 8><<<grid, 512, 0, s>>>(a);
+        else if (p->cap <= 8192) mass_select_kernel<1024, 8><<<grid, 1024, 0, s>>>(a);
+        else if (p->cap <= 16384) mass_select_kernel<1024, 16><<<grid, 1024, 0, s>>>(a);
+        else if (p->cap <= 32768) mass_select_kernel<1024, 32><<<grid, 1024, 0, s>>>(a);
+        else mass_select_long_kernel<<<grid, kMassThreads, 0, s>>>(a);
+    }
+    CRS_CHECK_LAUNCH();
+    return CRS_OK;
+}
+
+extern "C" int crs_cache_evict(const crs_cache_params *p, const crs_cache_state *st, int keep, const int32_t *idx,
+                               const int32_t *count, void *stream) {
+    int e = cache_validate(p);
+    if (e) return e;
+    if (keep < 1) return CRS_ERR_INVALID_ARG;
+    if ((e = cache_check_state(st))) return e;
+    if (!idx || !count) return CRS_ERR_INVALID_ARG;
+    const long long sh = (long long)p->n_seq * p->n_kv;
+    if (sh > 65535) return CRS_ERR_UNSUPPORTED;
+    // n kept slots of cap: at most min(n, cap - n) move
+    const int most = max(1, min(keep, p->cap / 2));
+    const dim3 grid((unsigned)ceil_div(most, kEvWarps * 32), (unsigned)sh);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const CacheDev c = cache_dev(p, st);
+    {
+        ProfScope _ps(K_CACHE_EVICT, s);
+        if (p->D == 128) cache_evict_kernel<128><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count);
+        else cache_evict_kernel<64><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count);
+    }
+    CRS_CHECK_LAUNCH();
+    return CRS_OK;
+}

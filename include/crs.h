@@ -7,6 +7,10 @@
  *   - a DSA-style lightning indexer with token top-k (crs_indexer_topk),
  *   - a COBS-style block-mass selector (crs_block_describe + crs_block_select),
  * and one attention kernel over explicit index lists (crs_sparse_attn).
+ * Around them, for decode: rotary positions (crs_rope), a paged K/V cache
+ * (crs_cache_append, _commit), attention over a prefix shared by the batch and the
+ * cached slots (crs_cache_attn), and eviction by accumulated attention weight
+ * (crs_mass_select, crs_cache_evict).
  *
  * Pages cited:
  *   [P1] PaperTrace 2.1.1 "哈希与聚类: 用内容建立稀疏注意力邻域"
@@ -591,6 +595,168 @@ int crs_sparse_attn(const crs_attn_params *p, const void *Q, const void *K, cons
                     const int64_t *kv_base, const int32_t *I, const uint8_t *key_valid,
                     const int32_t *q_pos, void *O, float *lse, void *ws, size_t ws_bytes,
                     void *stream);
+
+/* ====================================================================== *
+ * Rotary positions.  For the rot_dim dims [rot_begin, rot_begin + rot_dim) of a
+ * head, pair j (0 <= j < rot_dim / 2) of the token at position t turns by the
+ * angle t * inv_freq[j] and is scaled by mscale:
+ *   y_a = mscale (x_a cos - x_b sin),  y_b = mscale (x_b cos + x_a sin),
+ * with (a, b) = (rot_begin + j, rot_begin + rot_dim / 2 + j) (halves), or
+ * (rot_begin + 2 j, rot_begin + 2 j + 1) when interleaved.  The other dims are
+ * copied.  inverse turns by the negative angle: the transpose, which is also the
+ * gradient of the forward call.  Angles are formed and reduced in fp64 (a position
+ * past 2^20 times an fp32 frequency would lose the angle itself), the rotation is
+ * fp32, rounded once to the output type.  Stretching for long contexts is a matter
+ * of inv_freq and mscale.
+ * ====================================================================== */
+typedef struct {
+    int D;             /* head dim, 1..1024                                     */
+    int rot_begin;     /* first rotated dim, >= 0                               */
+    int rot_dim;       /* rotated dims, even, rot_begin + rot_dim <= D; 0: none  */
+    int interleaved;   /* 1: pairs (2j, 2j+1), 0: halves                        */
+    int inverse;       /* 1: the transpose                                      */
+    float mscale;      /* magnitude factor, 1 for plain rotation                */
+} crs_rope_params;
+
+/* x, y: n_tok rows of [n_heads, D] (dtype), token t at element t * x_stride
+ * (t * y_stride), strides >= n_heads * D; y may equal x (same stride: in place)
+ * but must not overlap it otherwise.  pos: [n_tok] int32; inv_freq: [rot_dim / 2]
+ * f64, radians per position (may be NULL when rot_dim is 0).  n_tok = 0 is a no-op.
+ * Vectors of up to 16 bytes are used as the sizes, strides and addresses allow. */
+int crs_rope(const crs_rope_params *p, int n_tok, int n_heads, int dtype, const void *x, int64_t x_stride,
+             const int32_t *pos, const double *inv_freq, void *y, int64_t y_stride, void *stream);
+
+/* ====================================================================== *
+ * K/V cache of a decode batch: pages behind a block table (as in
+ * crs_lsh_decode_*), with the slots of each KV head evicted independently.
+ * Slot j of sequence s lies in page block_table[s][j / page_size], row
+ * j % page_size; a head's slots hold whatever tokens it has kept, in any order
+ * (attention does not depend on it: keys are stored rotated).
+ *   k_pool, v_pool [n_pages, page_size, n_kv, D] bf16, 16-byte aligned;
+ *   block_table [n_seq, max_pages] int32; an entry outside [0, n_pages) that a
+ *     slot in use needs sets CRS_DEVERR_INDEX, and the slot is skipped;
+ *   pos  [n_seq, n_kv, cap] int32 (may be NULL): the position each slot's token has;
+ *   mass [n_seq, n_kv, cap] f32 (may be NULL): the attention weight each slot's
+ *     token has received;
+ *   seq_len [n_seq] int32: slots in use; next_pos [n_seq] int32: the position of
+ *     the next token (it keeps counting when slots are evicted).
+ * One step is append (new rows written at slots seq_len .., lengths unchanged),
+ * attend (sees them), commit (lengths advance, by fewer than were appended when
+ * drafted tokens are rejected); every call but commit can be repeated with the
+ * same result.  n_new: [n_seq] int32, the new tokens of each sequence, of which
+ * the first min(max(n_new, 0), n_tok) rows are used; NULL = n_tok for all.
+ * Lengths are read on the device, so a captured graph follows them.  A sequence
+ * whose new tokens pass cap sets CRS_DEVERR_CAPACITY and the tokens past it are
+ * dropped by all three calls.
+ * D = 64 or 128, n_seq <= 4096, cap <= max_pages * page_size,
+ * n_pages * page_size < 2^31 (else CRS_ERR_UNSUPPORTED).
+ * ====================================================================== */
+typedef struct {
+    int n_seq, n_kv, D;
+    int page_size;     /* slots per page, >= 1                                  */
+    int max_pages;     /* block_table row length                                */
+    int n_pages;       /* pages in the pools                                    */
+    int cap;           /* slots per sequence (row length of pos and mass)        */
+} crs_cache_params;
+
+typedef struct {
+    void *k_pool, *v_pool;
+    const int32_t *block_table;
+    int32_t *pos;
+    float *mass;
+    int32_t *seq_len, *next_pos;
+} crs_cache_state;
+
+/* Writes n_tok new rows per sequence: k (rotated, see crs_rope; r->D must equal
+ * p->D, r == NULL or rot_dim 0: as it is) and v at slots seq_len[s] + i, their
+ * pos = next_pos[s] + i and mass = 0; and q rotated into q_out when q is not NULL
+ * (rows of tokens past n_new are zero).  k, v [n_seq, n_tok, n_kv, D] bf16, q, q_out
+ * [n_seq, n_tok, n_q, D] bf16, token rows k_stride / v_stride / q_stride elements
+ * apart (so that all three may be slices of one projection; q_out is dense).
+ * Addresses 16-byte aligned, strides multiples of 8 (else CRS_ERR_INVALID_ARG);
+ * the rotated dims are handled in 16-byte pieces: rot_begin a multiple of 8,
+ * rot_dim of 16 (else CRS_ERR_UNSUPPORTED). */
+int crs_cache_append(const crs_cache_params *p, const crs_cache_state *st, const crs_rope_params *r,
+                     const double *inv_freq, int n_tok, const int32_t *n_new, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const void *q, int64_t q_stride, int n_q, void *q_out,
+                     void *stream);
+
+/* seq_len += n, next_pos += n with n = accepted[s] (NULL: n_tok) cut to
+ * [0, min(n_tok, cap - seq_len)]. */
+int crs_cache_commit(const crs_cache_params *p, const crs_cache_state *st, int n_tok, const int32_t *accepted,
+                     void *stream);
+
+/* ====================================================================== *
+ * Decode attention over a prefix that the whole batch shares and each sequence's
+ * own cached slots.  Row (s, i, g) (new token i of sequence s, query head g, KV
+ * head h = g / G, G = n_q / n_kv) sees all prefix_len prefix keys and the own slots
+ * j < seq_len[s] + i + 1 (its own and earlier new tokens):
+ *   O = sum_j softmax_j(scale * q . k_j) v_j over both sets, lse the natural log
+ * of the softmax's denominator.  The prefix K/V are read once for all rows: each
+ * KV head's queries of the whole batch form one tall tile.  A row past n_new, and a
+ * row that sees nothing, gets O = 0, lse = -inf.
+ * mass_out (may be NULL; may be st->mass: in place): for every slot j of
+ * sequence s below its length with the new tokens,
+ *   mass_out[s, h, j] = decay * mass[s, h, j] + sum over its rows of the weight of j;
+ * other slots are left as they were.
+ * Arithmetic: products of bf16 values summed in fp32; softmax statistics in fp32;
+ * the unnormalised weights enter the second product as bf16 when O is bf16 (an
+ * error below that of the output's own rounding) and as a bf16 value plus a bf16
+ * residual when O is f32.
+ * ====================================================================== */
+typedef struct {
+    crs_cache_params c;
+    int n_q;           /* query heads, a multiple of n_kv, n_q / n_kv <= 64      */
+    int n_tok;         /* query tokens per sequence, n_tok * n_q / n_kv <= 1024  */
+    int prefix_len;    /* shared keys, >= 0                                     */
+    int out_dtype;     /* crs_dtype of O                                        */
+    int want_mass;     /* 1: mass_out is given                                  */
+    float scale;       /* typically 1/sqrt(D)                                   */
+    float decay;       /* factor on the old mass, typically 1                   */
+} crs_cache_attn_params;
+
+/* Q: [n_seq, n_tok, n_q, D] bf16; prefix_k, prefix_v: [prefix_len, n_kv, D] bf16
+ * (16-byte aligned; may be NULL when prefix_len is 0).  O: [n_seq, n_tok, n_q, D]
+ * (16-byte aligned); lse: [n_seq, n_tok, n_q] f32 or NULL.  The workspace size
+ * depends on the current device's SM count: query it with the same device current.
+ * Calls that may overlap need workspaces of their own. */
+size_t crs_cache_attn_workspace_size(const crs_cache_attn_params *p);
+int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_state *st, const void *Q, const int32_t *n_new,
+                   const void *prefix_k, const void *prefix_v, void *O, float *lse, float *mass_out, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* ====================================================================== *
+ * Selection of the slots to keep by accumulated attention weight, next to the
+ * block selectors: for every (sequence, KV head) the min(keep, seq_len) slots
+ * j < seq_len[s] that rank first by (protected first, mass desc, slot asc).  A slot
+ * is protected when pos < sink_end or pos >= next_pos[s] - window (pos NULL: none
+ * is).  Lists are ascending, -1 padded, as crs_sparse_attn reads them with
+ * n_lists = n_kv; count[s] = min(keep, seq_len[s]).  A NaN mass sets
+ * CRS_DEVERR_NONFINITE and ranks below every number; seq_len is cut to [0, cap].
+ * ====================================================================== */
+typedef struct {
+    int n_seq, n_kv;
+    int cap;           /* row length of mass and pos                            */
+    int keep;          /* slots kept at most, 1..cap                            */
+    int sink_end;      /* positions below it are protected                      */
+    int window;        /* as are the last `window` positions, >= 0              */
+} crs_mass_select_params;
+
+/* mass [n_seq, n_kv, cap] f32; pos [n_seq, n_kv, cap] int32 or NULL; seq_len,
+ * next_pos [n_seq] int32 (next_pos may be NULL when pos is); idx [n_seq, n_kv, keep]
+ * int32; count [n_seq] int32. */
+int crs_mass_select(const crs_mass_select_params *p, const float *mass, const int32_t *pos, const int32_t *seq_len,
+                    const int32_t *next_pos, int32_t *idx, int32_t *count, void *stream);
+
+/* Evicts the slots that are not in the lists: with n = count[s], the r-th kept slot
+ * at or past n moves (K and V rows, pos, mass) to the r-th free slot below n, and
+ * seq_len[s] = n.  Only moved rows are read and written; kept slots below n stay,
+ * slots from n on keep their old contents, so the call can be repeated.  idx
+ * [n_seq, n_kv, keep] ascending, its first count[s] entries distinct slots of the
+ * sequence; count outside [0, min(keep, cap)] is cut to it, an entry outside [0, cap)
+ * sets CRS_DEVERR_INDEX and its row is not moved. */
+int crs_cache_evict(const crs_cache_params *p, const crs_cache_state *st, int keep, const int32_t *idx,
+                    const int32_t *count, void *stream);
 
 #ifdef __cplusplus
 }

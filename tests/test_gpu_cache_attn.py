@@ -1,0 +1,192 @@
+"""Decode attention over a shared prefix and the cached slots, against the 64-bit form.
+
+Tolerances.  With exact weights p_j (sum 1) and output O = sum p_j v_j, A = sum p_j |v_j|:
+ * a logit z (in log2 units, |z| <= Z) carries an fp32 error of at most
+   D 2^-24 sum|q_i k_i| scale log2(e) + 2 |z| 2^-24 (products exact, D additions, the scale) and
+   the subtraction of the maximum another |z - m| 2^-24; for normal inputs at scale 1/sqrt(D) this
+   is below 2^-16 relative in p, with ex2.approx's 2^-22.  The same error of the denominator
+   doubles it: 2^-15 A.
+ * sums of the weights and of p v: chains of at most 2^7 tensor-core steps per piece with at most
+   one fp32 step (2^-23, truncated) each, and a few joins: 2^-15 A.
+ * weights rounded to bf16 (half a step: 2^-8 relative before normalisation): 2^-8 A; split into
+   two bf16 values: the residual's half step, 2^-17 A at most.
+ * the output's own half step: 2^-8 |O| in bf16, 2^-24 |O| in f32.
+So |O' - O| <= A (2^-14 + 2^-17) for f32, A (2^-14 + 2^-8) + 2^-8 |O| for bf16; lse is off by
+2^-15 + |lse| 2^-22, an accumulated weight by 2^-14 of the sum of its contributions and 2^-23 of
+the result per addition.
+"""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TOL_F32 = 2.0 ** -14 + 2.0 ** -17
+
+
+def make(dev, n_seq, n_tok, n_q, n_kv, D, page, lens, prefix, seed, ragged=False, cap=None, poison=True,
+         spread=1.0):
+    """A cache with shuffled pages whose unused rows hold NaN and infinities."""
+    g = torch.Generator().manual_seed(seed)
+    cap = max(lens) + n_tok if cap is None else cap
+    max_pages = -(-cap // page)
+    n_pages = n_seq * max_pages + 3
+    r = lambda *sh: torch.randn(sh, generator=g).to(torch.bfloat16)  # noqa: E731
+    k, v = r(n_pages, page, n_kv, D) * spread, r(n_pages, page, n_kv, D)
+    table = torch.randperm(n_pages, generator=g)[: n_seq * max_pages].to(torch.int32).view(n_seq, max_pages)
+    n_new = torch.randint(0, n_tok + 1, (n_seq,), generator=g).to(torch.int32) if ragged else None
+    used = ref.n_used(n_new, n_tok, lens, cap)
+    if poison:
+        live = torch.zeros(n_pages, page, dtype=torch.bool)
+        for s in range(n_seq):
+            for j in range(lens[s] + used[s]):
+                live[int(table[s, j // page]), j % page] = True
+        k[~live] = float("nan")
+        v[~live] = float("inf")
+    q = r(n_seq, n_tok, n_q, D) * spread
+    pk, pv = (r(prefix, n_kv, D) * spread, r(prefix, n_kv, D)) if prefix else (None, None)
+    mass = torch.rand((n_seq, n_kv, cap), generator=g)
+    pos = torch.arange(cap, dtype=torch.int32).repeat(n_seq, n_kv, 1)
+    sl = torch.tensor(lens, dtype=torch.int32)
+    return dict(k=k, v=v, table=table, n_new=n_new, q=q, pk=pk, pv=pv, mass=mass, pos=pos, seq_len=sl, cap=cap,
+                used=used)
+
+
+def on(dev, c, crs):
+    d = {n: (t.to(dev) if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    cache = crs.KvCache(d["k"], d["v"], d["table"], d["seq_len"], d["seq_len"].clone(), pos=d["pos"], mass=d["mass"])
+    return d, cache
+
+
+def check(crs, dev, c, out_dtype, with_mass=True, decay=1.0, scale=None):
+    d, cache = on(dev, c, crs)
+    mo = d["mass"].clone() if with_mass else None
+    O, lse = cache.attend(d["q"], d["pk"], d["pv"], n_new=d["n_new"], out_dtype=out_dtype, mass_out=mo, decay=decay,
+                          scale=scale)
+    torch.cuda.synchronize()
+    assert crs.get_device_error() == 0
+    eO, el, em, A = ref.attend(c["q"], c["k"], c["v"], c["table"], c["seq_len"], c["cap"], c["n_new"], c["pk"],
+                               c["pv"], scale=scale, mass=c["mass"], decay=decay)
+    o = O.double().cpu()
+    tol = A * TOL_F32 + eO.abs() * 2.0 ** -24 if out_dtype == torch.float32 else \
+        A * (2.0 ** -14 + 2.0 ** -8) + eO.abs() * 2.0 ** -8
+    bad = ((o - eO).abs() > tol) | ~torch.isfinite(o)
+    assert not bad.any(), (int(bad.sum()), float((o - eO).abs().max()))
+    l = lse.double().cpu()
+    assert torch.equal(torch.isfinite(l), torch.isfinite(el))
+    f = torch.isfinite(el)
+    assert ((l[f] - el[f]).abs() <= 2.0 ** -15 + el[f].abs() * 2.0 ** -22).all()
+    assert torch.equal(l[~f], el[~f])
+    if with_mass:
+        got = mo.double().cpu()
+        tol = (em - decay * c["mass"].double()).abs() * 2.0 ** -14 + em.abs() * 2.0 ** -21
+        for s in range(len(c["used"])):
+            t = int(c["seq_len"][s]) + c["used"][s]
+            assert ((got - em).abs() <= tol)[s, :, :t].all()
+            assert torch.equal(mo[s, :, t:].cpu(), c["mass"][s, :, t:])     # other slots untouched
+    return d, cache, O, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n_q,n_kv", [(4, 4), (6, 2), (16, 1)])
+def test_own_slots_only(crs, cuda_dev, D, out_dtype, n_q, n_kv):
+    """No prefix; lengths of zero, one, and around the tile and page borders."""
+    c = make(cuda_dev, 6, 1, n_q, n_kv, D, 24, [0, 1, 62, 63, 64, 200], 0, 1)
+    check(crs, cuda_dev, c, out_dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("prefix", [1, 63, 64, 65, 300])
+def test_prefix_and_slots(crs, cuda_dev, D, out_dtype, prefix):
+    c = make(cuda_dev, 5, 1, 8, 2, D, 16, [0, 5, 64, 65, 129], prefix, 2)
+    check(crs, cuda_dev, c, out_dtype)
+
+
+@pytest.mark.parametrize("n_tok,n_q,n_kv", [(2, 4, 2), (5, 12, 4), (3, 40, 2), (7, 21, 3)])
+def test_several_new_tokens(crs, cuda_dev, n_tok, n_q, n_kv):
+    """Causal among the new tokens; more query rows than one tile; some sequences without any."""
+    for ragged in (False, True):
+        c = make(cuda_dev, 4, n_tok, n_q, n_kv, 128, 7, [0, 9, 63, 100], 77, 3, ragged=ragged)
+        check(crs, cuda_dev, c, torch.float32, decay=0.5)
+
+
+@pytest.mark.parametrize("n_seq,prefix", [(40, 700), (90, 130), (33, 1)])
+def test_many_sequences_share_the_prefix(crs, cuda_dev, n_seq, prefix):
+    """The prefix's query tile holds the whole batch, past 128 rows too."""
+    lens = [(7 * s) % 50 for s in range(n_seq)]
+    c = make(cuda_dev, n_seq, 1, 8, 2, 128, 32, lens, prefix, 4)
+    check(crs, cuda_dev, c, torch.bfloat16)
+    check(crs, cuda_dev, c, torch.float32, with_mass=False)
+
+
+def test_rows_that_see_nothing(crs, cuda_dev):
+    """No new token and no prefix: zeros, -inf, and the mass as it was."""
+    c = make(cuda_dev, 3, 2, 4, 2, 64, 16, [0, 5, 0], 0, 5)
+    c["n_new"] = torch.tensor([0, -3, 9], dtype=torch.int32)          # cut to 0, 0, 2
+    c["used"] = ref.n_used(c["n_new"], 2, [0, 5, 0], c["cap"])
+    c["k"], c["v"] = torch.nan_to_num(c["k"]), torch.nan_to_num(c["v"], posinf=0.0)
+    d, cache, O, lse = check(crs, cuda_dev, c, torch.float32)
+    assert (O[:2] == 0).all() and torch.isinf(lse[:2]).all()
+
+
+def test_wide_logits(crs, cuda_dev):
+    """Logits of some hundreds: the running maximum moves, far weights vanish."""
+    c = make(cuda_dev, 4, 1, 8, 2, 128, 16, [3, 70, 150, 500], 400, 6, spread=6.0)
+    d, cache = on(cuda_dev, c, crs)
+    O, lse = cache.attend(d["q"], d["pk"], d["pv"])
+    eO, el, _, A = ref.attend(c["q"], c["k"], c["v"], c["table"], c["seq_len"], c["cap"], None, c["pk"], c["pv"])
+    # |z| up to about 6 * 36 * sqrt(128) / sqrt(128) * 6 = 2^11 log2 units: 2^-24 2^11 D^(1/2) < 2^-9 relative in p
+    assert ((O.double().cpu() - eO).abs() <= A * 2.0 ** -8 + 1e-30).all()
+    assert ((lse.double().cpu() - el).abs() <= el.abs() * 2.0 ** -18 + 2.0 ** -15).all()
+
+
+def test_full_cache_drops_the_last_tokens(crs, cuda_dev):
+    c = make(cuda_dev, 2, 3, 4, 2, 64, 8, [14, 3], 20, 7, cap=16)
+    check(crs, cuda_dev, c, torch.float32)
+
+
+def test_bad_page_is_flagged_and_skipped(crs, cuda_dev):
+    """A block table entry outside the pool: its slots are skipped, the error word says so."""
+    c = make(cuda_dev, 1, 1, 2, 2, 64, 8, [20], 0, 8, poison=False)
+    c["table"][0, 1] = 10 ** 6
+    d, cache = on(cuda_dev, c, crs)
+    O, lse = cache.attend(d["q"])
+    torch.cuda.synchronize()
+    assert crs.get_device_error() == crs.DEVERR_INDEX
+    K = torch.stack([c["k"][int(c["table"][0, j // 8]), j % 8] for j in range(21) if j // 8 != 1]).double()
+    z = torch.einsum("jhd,hd->hj", K, c["q"][0, 0].double()) / 8.0
+    assert ((lse[0, 0].double().cpu() - torch.logsumexp(z, 1)).abs() <= 2.0 ** -14).all()
+
+
+def test_streams_graphs_and_repeats(crs, cuda_dev):
+    """The same bits again, on another stream, and from a captured graph after the lengths moved."""
+    c = make(cuda_dev, 7, 1, 8, 4, 128, 16, [0, 1, 30, 64, 77, 128, 300], 500, 9, poison=False, cap=320)
+    d, cache = on(cuda_dev, c, crs)
+    mo = d["mass"].clone()
+    O, lse = cache.attend(d["q"], d["pk"], d["pv"], mass_out=mo)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mo2 = d["mass"].clone()
+    s.wait_stream(torch.cuda.current_stream())
+    O2, lse2 = cache.attend(d["q"], d["pk"], d["pv"], mass_out=mo2, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(mo, mo2)
+    g = torch.cuda.CUDAGraph()
+    out, ls, m3 = torch.empty_like(O), torch.empty_like(lse), d["mass"].clone()
+    ws = torch.empty(max(cache._attn_ws.values()), dtype=torch.uint8, device=cuda_dev)
+    with torch.cuda.graph(g):
+        cache.attend(d["q"], d["pk"], d["pv"], out=out, lse=ls, mass_out=m3, workspace=ws)
+    d["seq_len"].copy_(torch.tensor([5, 0, 64, 63, 299, 1, 10], dtype=torch.int32))
+    g.replay()
+    mo4 = d["mass"].clone()
+    O4, lse4 = cache.attend(d["q"], d["pk"], d["pv"], mass_out=mo4)
+    torch.cuda.synchronize()
+    assert torch.equal(out, O4) and torch.equal(ls, lse4)
+    for s_ in range(7):
+        t = int(d["seq_len"][s_]) + 1
+        assert torch.equal(m3[s_, :, :t], mo4[s_, :, :t])

@@ -82,4 +82,27 @@ inline int cache_sms() {
     return sms;
 }
 
+// What the attention kernels and the merge of their partial results are given.
+struct CaArgs {
+    CacheDev c;
+    const __nv_bfloat16 *Q, *pk, *pv;
+    const int32_t *n_new;
+    int n_q, G, n_tok;
+    int M;             // query rows of one (sequence, KV head): n_tok * G
+    int RT;            // row tiles of an own item
+    int prefix_len;
+    int PT;            // key tiles of a prefix item of cache_attn_kernel (0: none)
+    int PRT;           // its row tiles, over n_seq * M rows
+    int grid;          // CTAs of cache_attn_kernel
+    int tc_splits;     // key splits of cache_prefix_kernel (0: not launched)
+    int tc_tiles;      // its row tiles per KV head, kPfRows rows each
+    float scale_log2, decay;
+    float *part_o, *part_ml;       // pieces: [piece][16][D], [piece][16][2] (m in log2 units, l)
+    float *tc_o, *tc_ml;           // [split][KV head][n_seq * M][D], [..][2]
+    float *logits;                 // [sequence][KV head][M][ls] log2-scaled, or null
+    int ls;
+    void *O;
+    float *lse, *mass_out;
+};
+
 }  // namespace crs

@@ -14,7 +14,6 @@
 #include <math.h>
 
 #include "cache.cuh"
-#include "tc.cuh"
 
 namespace crs {
 
@@ -24,29 +23,9 @@ constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaStages = 3;           // K/V tiles in the ring
 constexpr int kCaRows = 16;            // query rows of an item (M of mma.sync)
 constexpr int kCaRing = kCaStages + 1; // tiles whose row lists are kept
+constexpr int kCaTcRows = 16;          // rows per KV head above which the prefix goes to the tensor cores
 constexpr int kMgThreads = 256;
 constexpr int kMgSlots = 512;          // slots whose mass one CTA updates
-
-struct CaArgs {
-    CacheDev c;
-    const __nv_bfloat16 *Q, *pk, *pv;
-    const int32_t *n_new;
-    int n_q, G, n_tok;
-    int M;             // query rows of one (sequence, KV head): n_tok * G
-    int RT;            // row tiles of an own item
-    int prefix_len;
-    int PT;            // key tiles of a prefix item of cache_attn_kernel (0: none)
-    int PRT;           // its row tiles, over n_seq * M rows
-    int grid;          // CTAs of cache_attn_kernel
-    int tc_splits;     // key splits of cache_prefix_kernel (0: not launched)
-    float scale_log2, decay;
-    float *part_o, *part_ml;       // pieces: [piece][16][D], [piece][16][2] (m in log2 units, l)
-    float *tc_o, *tc_ml;           // [split][KV head][n_seq * M][D], [..][2]
-    float *logits;                 // [sequence][KV head][M][ls] log2-scaled, or null
-    int ls;
-    void *O;
-    float *lse, *mass_out;
-};
 
 // key tiles of a sequence's own items (none without a new token to ask)
 __device__ __forceinline__ int ca_tiles(const CaArgs &a, int s) {
@@ -669,7 +648,7 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int n
 
 // ----------------------------------------------------------------------------- host --
 struct CaPlan {
-    int grid, PT, PRT, RT, M, tc_splits;
+    int grid, PT, PRT, RT, M, tc_splits, tc_tiles;
     size_t part_o, part_ml, tc_o, tc_ml, logits, total;   // workspace offsets
     int ls;
 };
@@ -693,8 +672,14 @@ static CaPlan ca_plan(const crs_cache_attn_params *p) {
     q.M = p->n_tok * G;
     q.RT = ceil_div(q.M, kCaRows);
     q.grid = cache_sms() * (D == 128 ? ca_per_sm<128>() : ca_per_sm<64>());
-    q.tc_splits = 0;
-    q.PT = ceil_div(p->prefix_len, kCaKeys);
+    // the tensor-core pass pays off once the batch's rows exceed a tile or two of the plain one
+    const long long rows = (long long)p->c.n_seq * q.M;
+    const bool tc = p->prefix_len > 0 && rows > kCaTcRows;
+    q.tc_tiles = (int)ceil_div_ll(rows, kPfRows);
+    q.tc_splits = tc ? pf_splits(p->c.n_kv, q.tc_tiles, rows, D,
+                                 ceil_div(p->prefix_len, p->out_dtype == CRS_F32 ? 64 : 128), cache_sms())
+                     : 0;
+    q.PT = tc ? 0 : ceil_div(p->prefix_len, kCaKeys);
     q.PRT = q.PT > 0 ? ceil_div(p->c.n_seq * q.M, kCaRows) : 0;
     const size_t items = (size_t)p->c.n_kv * q.PRT + (size_t)p->c.n_seq * p->c.n_kv * q.RT;
     const size_t pieces = items + q.grid;
@@ -704,11 +689,11 @@ static CaPlan ca_plan(const crs_cache_attn_params *p) {
     at += up(pieces * kCaRows * D * 4);
     q.part_ml = at;
     at += up(pieces * kCaRows * 2 * 4);
-    const size_t tc = (size_t)q.tc_splits * p->c.n_kv * p->c.n_seq * q.M;
+    const size_t parts = (size_t)q.tc_splits * p->c.n_kv * p->c.n_seq * q.M;
     q.tc_o = at;
-    at += up(tc * D * 4);
+    at += up(parts * D * 4);
     q.tc_ml = at;
-    at += up(tc * 2 * 4);
+    at += up(parts * 2 * 4);
     q.ls = ceil_div(p->c.cap, kCaKeys) * kCaKeys;
     q.logits = at;
     if (p->want_mass) at += up((size_t)p->c.n_seq * p->c.n_kv * q.M * q.ls * 4);
@@ -782,6 +767,7 @@ extern "C" int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_st
     a.PRT = q.PRT;
     a.grid = q.grid;
     a.tc_splits = q.tc_splits;
+    a.tc_tiles = q.tc_tiles;
     a.scale_log2 = p->scale * kLog2e;
     a.decay = p->decay;
     a.part_o = reinterpret_cast<float *>(w + q.part_o);
@@ -794,6 +780,11 @@ extern "C" int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_st
     a.lse = lse;
     a.mass_out = mass_out;
     const bool f32 = p->out_dtype == CRS_F32;
+    if (a.tc_splits > 0) {
+        if (p->c.D == 128) e = f32 ? pf_launch<128, true>(a, s) : pf_launch<128, false>(a, s);
+        else e = f32 ? pf_launch<64, true>(a, s) : pf_launch<64, false>(a, s);
+        if (e) return e;
+    }
     if (p->c.D == 128) e = f32 ? ca_launch<128, true>(a, s) : ca_launch<128, false>(a, s);
     else e = f32 ? ca_launch<64, true>(a, s) : ca_launch<64, false>(a, s);
     if (e) return e;

@@ -1,0 +1,413 @@
+// The shared prefix's part of the decode attention on the tensor cores (tcgen05, TMA),
+// sm_100a.
+//
+// For one KV head the queries of the whole batch are one tall matrix (n_seq n_tok G
+// rows), so the prefix is read once for up to 256 of them and the two products run as
+// M = 128 tensor-core tiles.  A CTA takes (KV head, key split, 256 rows): two streams
+// of 128 rows share the K/V tiles of the split; with 128 rows or fewer both streams
+// hold the same rows and take the even and the odd key tiles, joined at the end.
+// Consecutive CTAs hold the row tiles of one key split, so the re-reads of its keys
+// meet in L2.
+//
+// Warps: 0-3 and 4-7 are the streams' softmax (one thread per row), 8 loads K/V tiles
+// by TMA into a ring, 9 issues the products.  Per stream and key tile: S = Q K^T to
+// tensor memory; the softmax threads read their rows, keep a running maximum that is
+// raised only when a row outgrows it by 2^8 (the sums are exact for any shift; O is
+// rescaled in tensor memory then, a rare event), and write P = 2^(S - m) over the S
+// columns; O += P V takes P from tensor memory.  While one stream's softmax runs, the
+// other's products do.
+//
+// P is bf16: one rounding for a bf16 output; three bf16 parts (24 bits) for an f32
+// output, over key tiles of 64 so that the parts fit beside S.
+#include "cache.cuh"
+#include "tc.cuh"
+
+namespace crs {
+
+constexpr int kPfThreads = 320;
+constexpr int kPfRows = 256;                     // rows of a CTA: two streams of 128
+constexpr uint64_t kPfWaitNs = 1000000000ull;    // 1 s: a wait that long means a fault
+constexpr float kPfSlack = 8.0f;                 // log2 units a logit may exceed the running shift
+
+template <int D, bool SPLIT> struct PfCfg {
+    static constexpr int kKeys = SPLIT ? 64 : 128;           // keys per tile
+    static constexpr int kParts = SPLIT ? 3 : 1;             // bf16 parts of P
+    static constexpr int kTile = kKeys * D * 2;              // bytes of a K or V tile
+    static constexpr int kQ = 128 * D * 2;                   // bytes of a Q tile
+    static constexpr int kStages = kTile >= 32768 ? 5 : 8;   // >= 5: see the order of use below
+    static constexpr int kSmem = 2 * kQ + kStages * kTile + 1024;
+    // tensor memory columns: S and the P over it, the parts of P that S cannot hold, O
+    static constexpr int kPCols = kKeys / 2;
+    static __host__ __device__ constexpr int s_col(int u) { return u * (SPLIT ? 128 : kKeys); }
+    static __host__ __device__ constexpr int o_col(int u) { return 256 + u * D; }
+};
+static_assert(PfCfg<128, false>::kSmem <= 232448 && PfCfg<128, true>::kSmem <= 232448, "shared memory of one CTA");
+
+struct PfBars {
+    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ float pf_max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// the query of row R of KV head h's tall matrix (null: no such token)
+__device__ __forceinline__ const __nv_bfloat16 *pf_query(const CaArgs &a, int h, int R) {
+    if (R >= a.c.n_seq * a.M) return nullptr;
+    const int s = R / a.M, r = R - s * a.M, i = r / a.G, g = r - i * a.G;
+    const int len = cache_len(a.c, s);
+    if (i >= cache_new(a.c, a.n_new, a.n_tok, s, len)) return nullptr;
+    return a.Q + (((size_t)s * a.n_tok + i) * a.n_q + h * a.G + g) * a.c.D;
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kPfThreads, 1)
+cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = PfCfg<D, SPLIT>;
+    constexpr int KT = C::kKeys;
+    extern __shared__ unsigned char pf_raw[];
+    __shared__ PfBars B;
+    unsigned char *sQ = pf_raw + ((1024u - (smem_u32(pf_raw) & 1023u)) & 1023u);
+    unsigned char *ring = sQ + 2 * C::kQ;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const int mt = blockIdx.x % a.tc_tiles, rest = blockIdx.x / a.tc_tiles;
+    const int split = rest % a.tc_splits, h = rest / a.tc_splits;
+    const int rows = a.c.n_seq * a.M;
+    const int row0 = mt * kPfRows;
+    const bool pair = rows - row0 <= 128;        // both streams hold the same rows
+    const int PT = (a.prefix_len + KT - 1) / KT;
+    const int t0 = (int)((long long)split * PT / a.tc_splits), t1 = (int)((long long)(split + 1) * PT / a.tc_splits);
+    const int n = t1 - t0;                       // key tiles of this split (>= 1)
+    auto count_of = [&](int u) { return pair ? (n + 1 - u) / 2 : n; };
+    auto tile_of = [&](int u, int i) { return pair ? 2 * i + u : i; };
+
+    if (tid == 0) {
+        tc::mbar_init(&B.q_full, 256);
+        for (int i = 0; i < C::kStages; ++i) {
+            tc::mbar_init(&B.kv_full[i], 1);
+            tc::mbar_init(&B.kv_empty[i], 1);
+        }
+        for (int u = 0; u < 2; ++u) {
+            tc::mbar_init(&B.s_full[u], 1);
+            tc::mbar_init(&B.p_full[u], 4);
+            tc::mbar_init(&B.o_full[u], 1);
+        }
+        tc::mbar_init(&B.drain, 1);
+        B.abort = 0;
+        tc::mbar_fence_init();
+    }
+    if (warp == 0) tc::tmem_alloc(&B.tmem, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = B.tmem;
+    volatile int *abort_flag = &B.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site, bool forceable) {
+        const bool ok = tc::mbar_wait_bounded(bar, parity & 1u, kPfWaitNs, K_CACHE_PREFIX, site, 10000u, forceable,
+                                              abort_flag);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+
+    if (warp == 8) {
+        // ---- K_0, V_0, K_1, V_1, ... through the ring
+        if (lane == 0) {
+            int issued = 0;
+            for (; issued < 2 * n; ++issued) {
+                const int st = issued % C::kStages, use = issued / C::kStages;
+                if (use > 0 && !wait(&B.kv_empty[st], (uint32_t)(use - 1), 2, false)) break;
+                tc::mbar_arrive_expect_tx(&B.kv_full[st], C::kTile);
+                const void *map = (issued & 1) ? (const void *)&tm_v : (const void *)&tm_k;
+                unsigned char *dst = ring + st * C::kTile;
+                const int key = (t0 + (issued >> 1)) * KT;
+#pragma unroll
+                for (int hh = 0; hh < D / 64; ++hh)
+                    tc::tma_load_3d(dst + hh * KT * 128, map, hh * 64, h, key, &B.kv_full[st]);
+            }
+            // no copy may still be on its way when the CTA leaves, after an early end too
+            for (int k = max(0, issued - C::kStages); k < issued; ++k)
+                tc::mbar_wait_bounded(&B.kv_full[k % C::kStages], (uint32_t)(k / C::kStages) & 1u, kPfWaitNs,
+                                      K_CACHE_PREFIX, 3);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- products.  Order of use of the ring: K_0 (K_1), then per step V_i, K_{i+1}
+        // of each stream; a tile is released when the last product that reads it completes.
+        if (lane == 0) {
+            constexpr uint32_t id_s = tc::idesc_bf16_f32(128, KT, 0, 0), id_o = tc::idesc_bf16_f32(128, D, 0, 1);
+            auto product_s = [&](int u, int i) {
+                const int k = 2 * tile_of(u, i), st = k % C::kStages;
+                if (!wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 4, false)) return false;
+                tc::fence_after();
+                const uint32_t qs = smem_u32(sQ) + (pair ? 0 : u * C::kQ), ks = smem_u32(ring + st * C::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int hh = kk >> 2, k4 = kk & 3;
+                    tc::mma_bf16(tmem + C::s_col(u),
+                                 tc::smem_desc(qs + hh * 128 * 128 + k4 * 32, 16, 1024, tc::kLayoutSW128),
+                                 tc::smem_desc(ks + hh * KT * 128 + k4 * 32, 16, 1024, tc::kLayoutSW128), id_s,
+                                 kk > 0 ? 1u : 0u);
+                }
+                tc::commit(&B.s_full[u]);
+                if (pair || u == 1) tc::commit(&B.kv_empty[st]);
+                return true;
+            };
+            bool ok = wait(&B.q_full, 0, 5, false);
+            tc::fence_after();
+            for (int u = 0; ok && u < 2; ++u)
+                if (count_of(u) > 0) ok = product_s(u, 0);
+            const int steps = count_of(0);       // the longer stream
+            for (int i = 0; ok && i < steps; ++i) {
+                for (int u = 0; ok && u < 2; ++u) {
+                    if (i >= count_of(u)) continue;
+                    const int k = 2 * tile_of(u, i) + 1, st = k % C::kStages;
+                    ok = wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 6, false) &&
+                         wait(&B.p_full[u], (uint32_t)i, 7, false);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t vs = smem_u32(ring + st * C::kTile);
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            tc::mma_f16_ts(tmem + C::o_col(u),
+                                           tmem + (uint32_t)(C::s_col(u) + part * C::kPCols + kk * 8),
+                                           tc::smem_desc(vs + kk * 16 * 128, KT * 128, 1024, tc::kLayoutSW128), id_o,
+                                           (i > 0 || kk > 0 || part > 0) ? 1u : 0u);
+                    if (i == count_of(u) - 1) tc::commit(&B.o_full[u]);
+                    if (pair || u == 1) tc::commit(&B.kv_empty[st]);
+                    if (i + 1 < count_of(u)) ok = product_s(u, i + 1);
+                }
+            }
+            if (!ok) {                           // let what was issued finish
+                tc::commit(&B.drain);
+                tc::mbar_wait_bounded(&B.drain, 0, kPfWaitNs, K_CACHE_PREFIX, 8);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: stream u, row r of its tile
+        const int u = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int row = row0 + (pair ? r : u * 128 + r);
+        {
+            // the stream's query rows (both streams fill half of the rows' chunks each when they
+            // share them); a negative scale goes into their signs, which is exact
+            const __nv_bfloat16 *q = pf_query(a, h, row);
+            const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+            unsigned char *dst = sQ + (pair ? 0 : u * C::kQ);
+            const int c0 = pair ? u * (D / 16) : 0, c1 = pair ? c0 + D / 16 : D / 8;
+            for (int c = c0; c < c1; ++c) {
+                uint4 w = q ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * 128 * 128 + tc::sw128(r, c & 7)) = w;
+            }
+            tc::fence_proxy_async();
+            tc::mbar_arrive(&B.q_full);
+        }
+        // never 0, so that a masked -inf stays one (the smallest normal leaves 2^(scale S) at 1)
+        const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+        const int cnt = count_of(u);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < cnt; ++i) {
+            ok = wait(&B.s_full[u], (uint32_t)i, 1, true);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            float v[KT];
+#pragma unroll
+            for (int c = 0; c < KT; c += 32)
+                tc::tmem_ld32(lanes + C::s_col(u) + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+            tc::tmem_ld_wait();
+            const int left = a.prefix_len - (t0 + tile_of(u, i)) * KT;
+            if (left < KT) {
+#pragma unroll
+                for (int e = 0; e < KT; ++e) v[e] = e < left ? v[e] : -INFINITY;
+            }
+            float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int e = 4; e < KT; e += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mx[q] = e + 4 < KT ? pf_max3(mx[q], v[e + q], v[e + 4 + q]) : fmax_nan(mx[q], v[e + q]);
+            const float top = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3])) * scale;
+            if (i == 0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, !(top <= m + kPfSlack))) {
+                const float mn = fmax_nan(m, top);
+                const float f = m == mn ? 1.0f : sa_ex2(m - mn);
+                m = mn;
+                l *= f;
+                // O of the earlier tiles is complete: S of this tile was issued after it
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t w[16];
+                    tc::tmem_ld16(lanes + C::o_col(u) + c, w);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                    tc::tmem_st16(lanes + C::o_col(u) + c, w);
+                }
+            }
+            const float sub = m == -INFINITY ? 0.0f : m;
+            const float2 neg = make_float2(-sub, -sub), sc2 = make_float2(scale, scale);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int c = 0; c < KT; c += 32) {
+                uint32_t w[C::kParts][16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float2 p = __ffma2_rn(make_float2(v[c + e], v[c + e + 1]), sc2, neg);
+                    p.x = sa_ex2(p.x);
+                    p.y = sa_ex2(p.y);
+                    sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], p);
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+                        w[part][e >> 1] = *reinterpret_cast<const uint32_t *>(&b);
+                        if (part + 1 < C::kParts) {
+                            const float2 back = __bfloat1622float2(b);
+                            p.x -= back.x;
+                            p.y -= back.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part)
+                    tc::tmem_st16(lanes + C::s_col(u) + part * C::kPCols + c / 2, w[part]);
+            }
+            const float2 t = __fadd2_rn(sum[0], sum[1]);
+            l += t.x + t.y;
+            tc::tmem_st_wait();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&B.p_full[u]);
+        }
+        // ---- the streams' results
+        if (ok)
+            for (int q = 0; ok && q < 2; ++q)
+                if (count_of(q) > 0) ok = wait(&B.o_full[q], 0, 9, false);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) tc::fence_after();
+        float4 *xo = reinterpret_cast<float4 *>(ring);                 // [D / 4][128]
+        float2 *xm = reinterpret_cast<float2 *>(ring + 128 * D * 4);   // [128]
+        if (pair) {
+            if (u == 1) {
+                xm[r] = make_float2(m, l);
+                if (ok && cnt > 0) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t w[16];
+                        tc::tmem_ld16(lanes + C::o_col(1) + c, w);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            xo[(c / 4 + e) * 128 + r] =
+                                make_float4(__uint_as_float(w[4 * e]), __uint_as_float(w[4 * e + 1]),
+                                            __uint_as_float(w[4 * e + 2]), __uint_as_float(w[4 * e + 3]));
+                    }
+                }
+            }
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        }
+        if (ok && !(pair && u == 1)) {
+            float f0 = 1.0f, f1 = 0.0f;
+            bool both = false;
+            if (pair && count_of(1) > 0) {
+                const float2 o = xm[r];
+                const float mn = fmax_nan(m, o.x);
+                f0 = m == mn ? 1.0f : sa_ex2(m - mn);
+                f1 = o.x == mn ? 1.0f : sa_ex2(o.x - mn);
+                l = l * f0 + o.y * f1;
+                m = mn;
+                both = true;
+            }
+            const size_t at = ((size_t)split * a.c.n_kv + h) * rows + row;
+            float *dst = a.tc_o + at * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                uint32_t w[16];
+                tc::tmem_ld16(lanes + C::o_col(u) + c, w);
+                tc::tmem_ld_wait();
+                if (row < rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float4 x = make_float4(__uint_as_float(w[4 * e]), __uint_as_float(w[4 * e + 1]),
+                                               __uint_as_float(w[4 * e + 2]), __uint_as_float(w[4 * e + 3]));
+                        if (both) {
+                            const float4 y = xo[(c / 4 + e) * 128 + r];
+                            x.x = x.x * f0 + y.x * f1;
+                            x.y = x.y * f0 + y.y * f1;
+                            x.z = x.z * f0 + y.z * f1;
+                            x.w = x.w * f0 + y.w * f1;
+                        }
+                        *reinterpret_cast<float4 *>(dst + c + e * 4) = x;
+                    }
+                }
+            }
+            if (row < rows) *reinterpret_cast<float2 *>(a.tc_ml + at * 2) = make_float2(m, l);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------- host --
+inline int pf_map(CUtensorMap *m, const void *base, int D, int n_kv, int keys, int box_keys) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tc::tensor_map_encoder();
+    if (!enc) return CRS_ERR_CUDA;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n_kv, (cuuint64_t)keys};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)n_kv * D * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_keys};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return CRS_ERR_CUDA;
+    return CRS_OK;
+}
+
+template <int D, bool SPLIT> int pf_launch(const CaArgs &a, cudaStream_t s) {
+    using C = PfCfg<D, SPLIT>;
+    CUtensorMap k, v;
+    int e = pf_map(&k, a.pk, D, a.c.n_kv, a.prefix_len, C::kKeys);
+    if (!e) e = pf_map(&v, a.pv, D, a.c.n_kv, a.prefix_len, C::kKeys);
+    if (e) return e;
+    CRS_TRY_CUDA(
+        cudaFuncSetAttribute(cache_prefix_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    ProfScope _ps(K_CACHE_PREFIX, s);
+    cache_prefix_kernel<D, SPLIT>
+        <<<(unsigned)(a.c.n_kv * a.tc_splits * a.tc_tiles), kPfThreads, C::kSmem, s>>>(a, k, v);
+    CRS_CHECK_LAUNCH();
+    return CRS_OK;
+}
+
+// Key splits: the grid's waves times a split's length, against the partial results that
+// every split writes and the merge reads.  In microseconds, measured on one B200: a key
+// tile of 128 takes about 1.5, a CTA's start and end 5, the partial results 3 TB/s.
+inline int pf_splits(int n_kv, int tiles, long long rows, int D, int PT, int sms) {
+    int best = 1;
+    double best_cost = 1e30;
+    for (int sp = 1; sp <= PT && sp <= 2 * sms; ++sp) {
+        const long long ctas = (long long)n_kv * tiles * sp;
+        const double waves = (double)((ctas + sms - 1) / sms);
+        const double cost = waves * (((PT + sp - 1) / sp) * 1.5 + 5.0) + (double)sp * rows * n_kv * D * 8 / 3e6;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = sp;
+        }
+    }
+    return best;
+}
+
+}  // namespace crs

@@ -87,8 +87,8 @@ int crs_get_device_diag(void *stream, uint32_t *out, int n);
 /* Test switch for the failure path of the bounded waits (the pages have no
  * counterpart: it exists to exercise this library's own fault handling).  While
  * on (on != 0, current device), the first mbarrier wait of the tensor-core LSH
- * kernels (the hash of crs_lsh_route and the chunk attention of crs_lsh_attn)
- * gives up at once, as a wait that ran out would: the kernel sets
+ * kernels (the hash of crs_lsh_route and the chunk attention of crs_lsh_attn) and
+ * of the shared-prefix pass of crs_cache_attn gives up at once, as a wait that ran out would: the kernel sets
  * CRS_DEVERR_TIMEOUT, records (kernel id, site 1) in the diagnostic record,
  * waits for the tensor-core work it issued, frees its tensor memory and
  * returns without writing its outputs (bucket ids, attention sums).  Turn it

@@ -190,3 +190,44 @@ def test_streams_graphs_and_repeats(crs, cuda_dev):
     for s_ in range(7):
         t = int(d["seq_len"][s_]) + 1
         assert torch.equal(m3[s_, :, :t], mo4[s_, :, :t])
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_seq,prefix", [(9, 127), (9, 128), (9, 129), (9, 1500), (70, 257), (130, 640)])
+def test_tensor_core_prefix(crs, cuda_dev, out_dtype, D, n_seq, prefix):
+    """36, 280 and 520 rows per KV head: one stream pair, several row tiles, one, few and many
+    key tiles, tails of one key."""
+    lens = [(5 * s) % 20 for s in range(n_seq)]
+    c = make(cuda_dev, n_seq, 1, 8, 2, D, 8, lens, prefix, 12)
+    check(crs, cuda_dev, c, out_dtype, with_mass=False)
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 1.0])
+def test_tensor_core_prefix_scales(crs, cuda_dev, scale):
+    """A negative and a zero scale; and logits wide enough to move the running shift."""
+    c = make(cuda_dev, 20, 1, 8, 2, 128, 8, [3] * 20, 900, 13, spread=1.5 if scale == 1.0 else 1.0)
+    d, cache = on(cuda_dev, c, crs)
+    O, lse = cache.attend(d["q"], d["pk"], d["pv"], scale=scale)
+    eO, el, _, A = ref.attend(c["q"], c["k"], c["v"], c["table"], c["seq_len"], c["cap"], None, c["pk"], c["pv"],
+                              scale=scale)
+    # |z| <= 2^8 log2 units here (1.5^2 * 128^(1/2) * 6 sigma * 1.44): 2^-24 2^8 a few times over
+    assert ((O.double().cpu() - eO).abs() <= A * 2.0 ** -13 + 1e-30).all()
+    assert ((lse.double().cpu() - el).abs() <= el.abs() * 2.0 ** -20 + 2.0 ** -14).all()
+
+
+def test_forced_wait_timeout_of_the_prefix_pass(crs, cuda_dev):
+    """The bounded waits' failure path: flagged, recorded, drained; the next call is right."""
+    c = make(cuda_dev, 9, 1, 8, 2, 128, 8, [4] * 9, 600, 14)
+    d, cache = on(cuda_dev, c, crs)
+    crs.get_device_error()
+    crs.get_device_diag()
+    try:
+        crs.debug_force_wait_timeout(True)
+        cache.attend(d["q"], d["pk"], d["pv"])
+        flags, diag = crs.get_device_error(), crs.get_device_diag()
+    finally:
+        crs.debug_force_wait_timeout(False)
+    assert flags & crs.DEVERR_TIMEOUT
+    assert diag[0] > 0 and diag[1] == 1
+    check(crs, cuda_dev, c, torch.float32)

@@ -14,6 +14,7 @@ Functions (same names as the C entry points, without the ``crs_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -199,19 +200,20 @@ _sig("crs_sparse_attn", ctypes.c_int, [ctypes.POINTER(AttnParams), _VP, _VP, _VP
                                         _VP, _VP, _VP, _VP, _SZ, _VP])
 
 _I64 = ctypes.c_int64
-_sig("crs_rope", ctypes.c_int, [ctypes.POINTER(RopeParams), ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP, _I64, _VP,
-                                _VP, _VP, _I64, _VP])
-_sig("crs_cache_append", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState),
-                                        ctypes.POINTER(RopeParams), _VP, ctypes.c_int, _VP, _VP, _I64, _VP, _I64, _VP,
-                                        _I64, ctypes.c_int, _VP, _VP])
-_sig("crs_cache_commit", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState), ctypes.c_int, _VP,
-                                        _VP])
+_c_rope = _sig("crs_rope", ctypes.c_int, [ctypes.POINTER(RopeParams), ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP,
+                                          _I64, _VP, _VP, _VP, _I64, _VP])
+_c_append = _sig("crs_cache_append", ctypes.c_int,
+                 [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState), ctypes.POINTER(RopeParams), _VP,
+                  ctypes.c_int, _VP, _VP, _I64, _VP, _I64, _VP, _I64, ctypes.c_int, _VP, _VP])
+_c_commit = _sig("crs_cache_commit", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState),
+                                                    ctypes.c_int, _VP, _VP])
 _sig("crs_cache_attn_workspace_size", _SZ, [ctypes.POINTER(CacheAttnParams)])
-_sig("crs_cache_attn", ctypes.c_int, [ctypes.POINTER(CacheAttnParams), ctypes.POINTER(CacheState), _VP, _VP, _VP, _VP,
-                                      _VP, _VP, _VP, _VP, _SZ, _VP])
-_sig("crs_mass_select", ctypes.c_int, [ctypes.POINTER(MassSelectParams), _VP, _VP, _VP, _VP, _VP, _VP, _VP])
-_sig("crs_cache_evict", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState), ctypes.c_int, _VP,
-                                       _VP, _VP])
+_c_attn = _sig("crs_cache_attn", ctypes.c_int, [ctypes.POINTER(CacheAttnParams), ctypes.POINTER(CacheState), _VP, _VP,
+                                                _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP])
+_c_mass_select = _sig("crs_mass_select", ctypes.c_int, [ctypes.POINTER(MassSelectParams), _VP, _VP, _VP, _VP, _VP, _VP,
+                                                        _VP])
+_c_evict = _sig("crs_cache_evict", ctypes.c_int, [ctypes.POINTER(CacheParams), ctypes.POINTER(CacheState),
+                                                  ctypes.c_int, _VP, _VP, _VP])
 
 _sig("crs_profile_set", ctypes.c_int, [ctypes.c_int])
 _sig("crs_profile_collect", ctypes.c_int, [ctypes.POINTER(KernelStat), ctypes.c_int,
@@ -969,25 +971,57 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, factor: float = 1.0, scal
     return f.to(device)
 
 
-def _on_current(t: torch.Tensor, name: str):
-    """The launch goes to the current device: a tensor of another one is refused."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+# The calls from here on are made once per layer and token: their checks are one test
+# per tensor on the good path, and only a failed test looks for the reason.
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape, device):
-    """A tensor whose last two dims are dense and whose leading dims are evenly spaced
-    token rows (a slice of a wider projection, say); returns the row stride in elements."""
+def _good(t, dtype, shape, dev: int) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+        t.is_contiguous()
+
+
+def _want(t, name: str, dtype, shape, dev: int):
+    """A contiguous tensor of this dtype and shape on device dev; its address."""
+    if not _good(t, dtype, shape, dev):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _current(t: torch.Tensor, name: str) -> int:
+    """t's device, which must be the current one: the launch goes there."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _get_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_get_device()}")
+    return dev
+
+
+def _launch_stream(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """A tensor whose last two dims are dense and whose leading dims are evenly spaced
+    token rows (a slice of a wider projection, say); returns the row stride in elements."""
+    if _good(t, dtype, shape, dev):
+        return shape[-1] * shape[-2]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return shape[-1] * shape[-2]
     st, sz = t.stride(), t.shape
     row = step = None
     for d in range(t.dim() - 3, -1, -1):
@@ -1013,27 +1047,37 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_rope_params = functools.lru_cache(maxsize=256)(
+    lambda D, begin, rot, inter, inverse, mscale: RopeParams(D, begin, rot, inter, inverse, mscale))
+
+
 def rope(x, pos, inv_freq, *, rot_begin: int = 0, interleaved: bool = False, mscale: float = 1.0,
          inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [n_tok, n_heads, D] bf16 or f32 (token rows may be strided), pos
     [n_tok] int32, inv_freq [rot_dim / 2] float64 -> the rotated x (new, or out; out=x
     rotates in place).  inverse=True applies the transpose: the gradient of the call."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+    dev = _current(x, "x")
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("rope: x [n_tok, n_heads, D] expected")
-    n_tok, heads, D = x.shape
+    n_tok, heads, D = shape
+    dtype = x.dtype
     code = _dtype_code(x)
-    _need(pos, "pos", torch.int32, (n_tok,))
-    _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),))
-    _on_current(pos, "pos")
-    _on_current(inv_freq, "inv_freq")
-    xs = _rows(x, "x", x.dtype, x.shape, pos.device)
+    half = inv_freq.numel()
+    pos_at = _want(pos, "pos", torch.int32, (n_tok,), dev)
+    freq_at = _want(inv_freq, "inv_freq", torch.float64, (half,), dev)
+    xs = _rows(x, "x", dtype, shape, dev)
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream)
-    ys = _rows(out, "out", x.dtype, x.shape, pos.device)
-    p = RopeParams(D, int(rot_begin), 2 * inv_freq.numel(), int(interleaved), int(inverse), float(mscale))
-    st = _lib.crs_rope(ctypes.byref(p), n_tok, heads, code, x.data_ptr(), xs, pos.data_ptr(), inv_freq.data_ptr(),
-                       out.data_ptr(), ys, _stream(stream))
-    _check("crs_rope", st)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format) if stream is None else \
+            _empty(shape, dtype, x.device, stream)
+        ys = heads * D
+    else:
+        ys = _rows(out, "out", dtype, shape, dev)
+    p = _rope_params(D, int(rot_begin), 2 * half, int(interleaved), int(inverse), float(mscale))
+    st = _c_rope(p, n_tok, heads, code, x.data_ptr(), xs, pos_at, freq_at, out.data_ptr(), ys,
+                 _launch_stream(stream, dev))
+    if st:
+        raise CrsError("crs_rope", st)
     return out
 
 
@@ -1044,28 +1088,28 @@ def mass_select(mass, seq_len, keep: int, *, pos=None, next_pos=None, sink_end: 
     mass [n_seq, n_kv, cap] f32 -> (idx [n_seq, n_kv, keep] int32 ascending, -1 pad; count
     [n_seq] int32).  With pos [n_seq, n_kv, cap] and next_pos [n_seq] (int32), slots of
     positions below sink_end and of the last `window` positions are kept first."""
-    _need(mass, "mass", torch.float32)
-    _on_current(mass, "mass")
-    if mass.dim() != 3:
+    dev = _current(mass, "mass")
+    shape = mass.shape
+    if len(shape) != 3:
         raise ValueError("mass_select: mass [n_seq, n_kv, cap] expected")
-    n_seq, n_kv, cap = mass.shape
-    for t, nm, shape in ((seq_len, "seq_len", (n_seq,)), (pos, "pos", (n_seq, n_kv, cap)),
-                         (next_pos, "next_pos", (n_seq,))):
-        if t is not None or nm == "seq_len":
-            _need(t, nm, torch.int32, shape)
-            _on_current(t, nm)
-    if (sink_end > 0 or window > 0) and pos is None:
+    n_seq, n_kv, cap = shape
+    mass_at = _want(mass, "mass", torch.float32, shape, dev)
+    len_at = _want(seq_len, "seq_len", torch.int32, (n_seq,), dev)
+    pos_at = next_at = None
+    if pos is not None:
+        pos_at = _want(pos, "pos", torch.int32, shape, dev)
+        next_at = _want(next_pos, "next_pos", torch.int32, (n_seq,), dev)
+    elif sink_end > 0 or window > 0:
         raise ValueError("mass_select: sink_end and window need pos and next_pos")
     if idx is None:
         idx = _empty((n_seq, n_kv, keep), torch.int32, mass.device, stream)
     if count is None:
         count = _empty((n_seq,), torch.int32, mass.device, stream)
-    _need(idx, "idx", torch.int32, (n_seq, n_kv, keep))
-    _need(count, "count", torch.int32, (n_seq,))
     p = MassSelectParams(n_seq, n_kv, cap, int(keep), int(sink_end), int(window))
-    st = _lib.crs_mass_select(ctypes.byref(p), _ptr(mass), _ptr(pos), _ptr(seq_len), _ptr(next_pos), _ptr(idx),
-                              _ptr(count), _stream(stream))
-    _check("crs_mass_select", st)
+    st = _c_mass_select(p, mass_at, pos_at, len_at, next_at, _want(idx, "idx", torch.int32, (n_seq, n_kv, keep), dev),
+                        _want(count, "count", torch.int32, (n_seq,), dev), _launch_stream(stream, dev))
+    if st:
+        raise CrsError("crs_mass_select", st)
     return idx, count
 
 
@@ -1115,7 +1159,8 @@ class KvCache:
         self.p = CacheParams(n_seq, n_kv, D, page_size, max_pages, n_pages, cap)
         self.st = CacheState(*(t.data_ptr() if t is not None else None
                                for t in (k_pool, v_pool, block_table, pos, mass, seq_len, next_pos)))
-        self._attn_ws = {}
+        self._dev = k_pool.get_device()
+        self._attn = {}              # parameters and workspace size by problem
 
     @classmethod
     def empty(cls, n_seq, n_kv, max_len, D=128, page_size=64, first_pos=0, track=True, device="cuda"):
@@ -1132,12 +1177,13 @@ class KvCache:
         mass = torch.zeros((n_seq, n_kv, max_len), dtype=torch.float32, device=device) if track else None
         return cls(kv[0], kv[1], table, ln, nxt, pos=pos, mass=mass)
 
+    def _here(self) -> int:
+        if self._dev != _get_device():
+            raise ValueError(f"the cache is on cuda:{self._dev}, the current device is cuda:{_get_device()}")
+        return self._dev
+
     def _counts(self, n_new, name):
-        if n_new is not None:
-            _need(n_new, name, torch.int32, (self.n_seq,))
-            _on_current(n_new, name)
-            return n_new.data_ptr()
-        return None
+        return None if n_new is None else _want(n_new, name, torch.int32, (self.n_seq,), self._dev)
 
     def append(self, k, v, q=None, inv_freq=None, n_new=None, *, rot_begin=0, interleaved=False, mscale=1.0,
                q_out=None, stream=None):
@@ -1145,46 +1191,48 @@ class KvCache:
         strided), k rotated by the positions next_pos + i when inv_freq is given; returns q
         [n_seq, n_tok, n_q, D] rotated likewise (None without q).  n_new [n_seq] int32: how
         many of each sequence's padded tokens exist.  Lengths advance in commit."""
-        _on_current(self.k_pool, "the cache")
+        dev = self._here()
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("append: k [n_seq, n_tok, n_kv, D] expected")
-        n_tok = k.shape[1]
-        shape = (self.n_seq, n_tok, self.n_kv, self.D)
-        ks = _rows(k, "k", torch.bfloat16, shape, self.device)
-        vs = _rows(v, "v", torch.bfloat16, shape, self.device)
+        n_tok, D = k.shape[1], self.D
+        shape = (self.n_seq, n_tok, self.n_kv, D)
+        ks = _rows(k, "k", torch.bfloat16, shape, dev)
+        vs = _rows(v, "v", torch.bfloat16, shape, dev)
         qs = n_q = 0
+        q_at = out_at = r = fp = None
         if q is not None:
+            if not isinstance(q, torch.Tensor) or q.dim() != 4:
+                raise ValueError("append: q [n_seq, n_tok, n_q, D] expected")
             n_q = q.shape[2]
-            qshape = (self.n_seq, n_tok, n_q, self.D)
-            qs = _rows(q, "q", torch.bfloat16, qshape, self.device)
+            qshape = (self.n_seq, n_tok, n_q, D)
+            qs = _rows(q, "q", torch.bfloat16, qshape, dev)
             if q_out is None:
-                q_out = _empty(qshape, torch.bfloat16, self.device, stream)
-            _need(q_out, "q_out", torch.bfloat16, qshape)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
+                    _empty(qshape, torch.bfloat16, self.device, stream)
+            q_at, out_at = q.data_ptr(), _want(q_out, "q_out", torch.bfloat16, qshape, dev)
         elif q_out is not None:
             raise ValueError("append: q_out without q")
-        r = fp = None
         if inv_freq is not None:
-            _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),))
-            _on_current(inv_freq, "inv_freq")
-            r = ctypes.byref(RopeParams(self.D, int(rot_begin), 2 * inv_freq.numel(), int(interleaved), 0,
-                                        float(mscale)))
-            fp = inv_freq.data_ptr()
-        st = _lib.crs_cache_append(ctypes.byref(self.p), ctypes.byref(self.st), r, fp, n_tok,
-                                   self._counts(n_new, "n_new"), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, n_q,
-                                   _ptr(q_out), _stream(stream))
-        _check("crs_cache_append", st)
+            half = inv_freq.numel()
+            fp = _want(inv_freq, "inv_freq", torch.float64, (half,), dev)
+            r = _rope_params(D, int(rot_begin), 2 * half, int(interleaved), 0, float(mscale))
+        st = _c_append(self.p, self.st, r, fp, n_tok, self._counts(n_new, "n_new"), k.data_ptr(), ks, v.data_ptr(), vs,
+                       q_at, qs, n_q, out_at, _launch_stream(stream, dev))
+        if st:
+            raise CrsError("crs_cache_append", st)
         return q_out
 
     def commit(self, n, n_tok=None, stream=None):
         """Advance the lengths by n: a number, or accepted tokens per sequence ([n_seq] int32,
         of at most n_tok appended)."""
-        _on_current(self.k_pool, "the cache")
+        dev = self._here()
         accepted = None
         if isinstance(n, torch.Tensor):
             accepted = self._counts(n, "accepted")
             n = 0x7fffffff if n_tok is None else n_tok
-        st = _lib.crs_cache_commit(ctypes.byref(self.p), ctypes.byref(self.st), int(n), accepted, _stream(stream))
-        _check("crs_cache_commit", st)
+        st = _c_commit(self.p, self.st, int(n), accepted, _launch_stream(stream, dev))
+        if st:
+            raise CrsError("crs_cache_commit", st)
 
     def attend(self, q, prefix_k=None, prefix_v=None, n_new=None, *, scale=None, out_dtype=torch.float32, out=None,
                lse=None, mass_out=None, decay=1.0, workspace=None, stream=None):
@@ -1192,50 +1240,61 @@ class KvCache:
         each sequence's slots, the appended tokens included (causally) -> (O in out_dtype,
         f32 or bf16, lse).  mass_out [n_seq, n_kv, cap] f32 (self.mass: in place) receives
         decay * self.mass plus the weights the slots got."""
-        _on_current(self.k_pool, "the cache")
-        _need(q, "q", torch.bfloat16)
-        if q.dim() != 4 or q.shape[0] != self.n_seq or q.shape[3] != self.D:
-            raise ValueError(f"q must be [{self.n_seq}, n_tok, n_q, {self.D}], got {tuple(q.shape)}")
+        dev = self._here()
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError(f"q must be [{self.n_seq}, n_tok, n_q, {self.D}]")
         n_tok, n_q = q.shape[1], q.shape[2]
-        plen = 0
-        if (prefix_k is None) != (prefix_v is None):
-            raise ValueError("attend: prefix_k and prefix_v go together")
-        if prefix_k is not None:
+        shape = (self.n_seq, n_tok, n_q, self.D)
+        q_at = _want(q, "q", torch.bfloat16, shape, dev)
+        plen, pk_at, pv_at, mass_at = 0, None, None, None
+        if prefix_k is not None and prefix_v is not None:
             plen = prefix_k.shape[0]
-            _need(prefix_k, "prefix_k", torch.bfloat16, (plen, self.n_kv, self.D))
-            _need(prefix_v, "prefix_v", torch.bfloat16, (plen, self.n_kv, self.D))
+            pk_at = _want(prefix_k, "prefix_k", torch.bfloat16, (plen, self.n_kv, self.D), dev)
+            pv_at = _want(prefix_v, "prefix_v", torch.bfloat16, (plen, self.n_kv, self.D), dev)
+        elif prefix_k is not prefix_v:
+            raise ValueError("attend: prefix_k and prefix_v go together")
         if out is None:
-            out = _empty(q.shape, out_dtype, self.device, stream)
-        _need(out, "out", None, q.shape)
+            out = torch.empty_like(q) if out_dtype is torch.bfloat16 and stream is None else \
+                _empty(shape, out_dtype, self.device, stream)
         code = _dtype_code(out)
+        out_at = _want(out, "out", out.dtype, shape, dev)
         if lse is None:
-            lse = _empty((self.n_seq, n_tok, n_q), torch.float32, self.device, stream)
-        _need(lse, "lse", torch.float32, (self.n_seq, n_tok, n_q))
+            lse = _empty(shape[:3], torch.float32, self.device, stream)
+        lse_at = _want(lse, "lse", torch.float32, shape[:3], dev)
         if mass_out is not None:
             if self.mass is None:
                 raise ValueError("attend: mass_out needs a cache that tracks mass")
-            _need(mass_out, "mass_out", torch.float32, (self.n_seq, self.n_kv, self.cap))
-        for t, nm in ((q, "q"), (prefix_k, "prefix_k"), (prefix_v, "prefix_v"), (out, "out"), (lse, "lse"),
-                      (mass_out, "mass_out"), (workspace, "workspace")):
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{nm} must be on {self.device}, got {t.device}")
+            mass_at = _want(mass_out, "mass_out", torch.float32, (self.n_seq, self.n_kv, self.cap), dev)
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
-        p = CacheAttnParams(self.p, n_q, n_tok, plen, code, int(mass_out is not None), float(scale), float(decay))
-        key = (n_q, n_tok, plen, code, mass_out is not None)
-        nbytes = self._attn_ws.get(key)
-        if nbytes is None:
-            nbytes = self._attn_ws[key] = int(_lib.crs_cache_attn_workspace_size(ctypes.byref(p)))
+        key = (n_q, n_tok, plen, code, mass_at is None, scale, decay)
+        known = self._attn.get(key)
+        if known is None:
+            p = CacheAttnParams(self.p, n_q, n_tok, plen, code, int(mass_at is not None), float(scale), float(decay))
+            if len(self._attn) >= 256:           # a prefix that grows leaves entries behind
+                self._attn.clear()
+            known = self._attn[key] = (p, max(16, int(_lib.crs_cache_attn_workspace_size(ctypes.byref(p)))))
+        p, nbytes = known
         if workspace is None:
-            workspace = _empty((max(nbytes, 16),), torch.uint8, self.device, stream)
-        elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous():
-            raise ValueError(f"workspace too small: need {nbytes} contiguous bytes")
-        st = _lib.crs_cache_attn(ctypes.byref(p), ctypes.byref(self.st), q.data_ptr(), self._counts(n_new, "n_new"),
-                                 _ptr(prefix_k) if plen else None, _ptr(prefix_v) if plen else None, out.data_ptr(),
-                                 lse.data_ptr(), _ptr(mass_out), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
-        _check("crs_cache_attn", st)
+            workspace = _empty((nbytes,), torch.uint8, self.device, stream)
+        else:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+            have = workspace.numel() * workspace.element_size()
+            if have < nbytes:
+                raise ValueError(f"workspace too small: need {nbytes} bytes")
+            nbytes = have
+        st = _c_attn(p, self.st, q_at, self._counts(n_new, "n_new"), pk_at if plen else None, pv_at if plen else None,
+                     out_at, lse_at, mass_at, workspace.data_ptr(), nbytes, _launch_stream(stream, dev))
+        if st:
+            raise CrsError("crs_cache_attn", st)
         return out, lse
+
+    def attend_workspace_size(self, n_q, n_tok=1, prefix_len=0, out_dtype=torch.float32, with_mass=False) -> int:
+        """Bytes of workspace that attend needs (to pass one that is kept, in a captured graph say)."""
+        p = CacheAttnParams(self.p, int(n_q), int(n_tok), int(prefix_len),
+                            CRS_BF16 if out_dtype is torch.bfloat16 else CRS_F32, int(with_mass), 1.0, 1.0)
+        return int(_lib.crs_cache_attn_workspace_size(ctypes.byref(p)))
 
     def select(self, keep, *, sink_end=0, window=0, idx=None, count=None, stream=None):
         """mass_select on this cache's weights, positions and lengths."""
@@ -1248,11 +1307,12 @@ class KvCache:
     def evict(self, idx, count, stream=None):
         """Keep only the listed slots of each KV head (idx [n_seq, n_kv, keep] ascending, count
         [n_seq], from select): later ones move into the freed slots, seq_len becomes count."""
-        _on_current(self.k_pool, "the cache")
-        _need(idx, "idx", torch.int32)
-        if idx.dim() != 3 or idx.shape[0] != self.n_seq or idx.shape[1] != self.n_kv:
-            raise ValueError(f"idx must be [{self.n_seq}, {self.n_kv}, keep], got {tuple(idx.shape)}")
-        _on_current(idx, "idx")
-        st = _lib.crs_cache_evict(ctypes.byref(self.p), ctypes.byref(self.st), idx.shape[2], idx.data_ptr(),
-                                  self._counts(count, "count"), _stream(stream))
-        _check("crs_cache_evict", st)
+        dev = self._here()
+        if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
+            raise ValueError(f"idx must be [{self.n_seq}, {self.n_kv}, keep]")
+        keep = idx.shape[2]
+        idx_at = _want(idx, "idx", torch.int32, (self.n_seq, self.n_kv, keep), dev)
+        st = _c_evict(self.p, self.st, keep, idx_at, _want(count, "count", torch.int32, (self.n_seq,), dev),
+                      _launch_stream(stream, dev))
+        if st:
+            raise CrsError("crs_cache_evict", st)

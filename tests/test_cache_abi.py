@@ -156,7 +156,7 @@ def test_binding_refuses_cpu_tensors_and_bad_frequencies(crs):
 
 def test_row_strides(crs):
     """Token rows may be slices of a wider projection; anything else is refused."""
-    dev = torch.device("cpu")
+    dev = torch.zeros(1).get_device()
     t = torch.zeros(3, 5, 8, 64, dtype=torch.bfloat16)
     rows = lambda v: crs._rows(v, "v", torch.bfloat16, v.shape, dev)  # noqa: E731
     assert rows(t) == 8 * 64

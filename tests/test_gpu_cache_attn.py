@@ -178,7 +178,7 @@ def test_streams_graphs_and_repeats(crs, cuda_dev):
     assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(mo, mo2)
     g = torch.cuda.CUDAGraph()
     out, ls, m3 = torch.empty_like(O), torch.empty_like(lse), d["mass"].clone()
-    ws = torch.empty(max(cache._attn_ws.values()), dtype=torch.uint8, device=cuda_dev)
+    ws = torch.empty(cache.attend_workspace_size(8, 1, 500, with_mass=True), dtype=torch.uint8, device=cuda_dev)
     with torch.cuda.graph(g):
         cache.attend(d["q"], d["pk"], d["pv"], out=out, lse=ls, mass_out=m3, workspace=ws)
     d["seq_len"].copy_(torch.tensor([5, 0, 64, 63, 299, 1, 10], dtype=torch.int32))

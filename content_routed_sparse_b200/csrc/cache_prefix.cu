@@ -73,7 +73,8 @@ cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __
     __shared__ PfBars B;
     unsigned char *sQ = pf_raw + ((1024u - (smem_u32(pf_raw) & 1023u)) & 1023u);
     unsigned char *ring = sQ + 2 * C::kQ;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);      // uniform for the compiler too
 
     const int mt = blockIdx.x % a.tc_tiles, rest = blockIdx.x / a.tc_tiles;
     const int split = rest % a.tc_splits, h = rest / a.tc_splits;
@@ -138,58 +139,63 @@ cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __
     } else if (warp == 9) {
         // ---- products.  Order of use of the ring: K_0 (K_1), then per step V_i, K_{i+1}
         // of each stream; a tile is released when the last product that reads it completes.
-        if (lane == 0) {
-            constexpr uint32_t id_s = tc::idesc_bf16_f32(128, KT, 0, 0), id_o = tc::idesc_bf16_f32(128, D, 0, 1);
-            auto product_s = [&](int u, int i) {
-                const int k = 2 * tile_of(u, i), st = k % C::kStages;
-                if (!wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 4, false)) return false;
-                tc::fence_after();
-                const uint32_t qs = smem_u32(sQ) + (pair ? 0 : u * C::kQ), ks = smem_u32(ring + st * C::kTile);
+        constexpr uint32_t id_s = tc::idesc_bf16_f32(128, KT, 0, 0), id_o = tc::idesc_bf16_f32(128, D, 0, 1);
+        const uint64_t q_desc = tc::smem_desc(smem_u32(sQ), 16, 1024, tc::kLayoutSW128);
+        const uint64_t k_desc = tc::smem_desc(smem_u32(ring), 16, 1024, tc::kLayoutSW128);
+        const uint64_t v_desc = tc::smem_desc(smem_u32(ring), KT * 128, 1024, tc::kLayoutSW128);
+        auto all_wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
+            return __all_sync(0xffffffffu, wait(bar, parity, site, false)) != 0;
+        };
+        auto product_s = [&](int u, int i) {
+            const int k = 2 * tile_of(u, i), st = k % C::kStages;
+            if (!all_wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 4)) return false;
+            tc::fence_after();
+            const uint64_t qd = q_desc + (uint64_t)(pair ? 0 : u * (C::kQ >> 4));
+            const uint64_t kd = k_desc + (uint64_t)(st * (C::kTile >> 4));
+            if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int hh = kk >> 2, k4 = kk & 3;
-                    tc::mma_bf16(tmem + C::s_col(u),
-                                 tc::smem_desc(qs + hh * 128 * 128 + k4 * 32, 16, 1024, tc::kLayoutSW128),
-                                 tc::smem_desc(ks + hh * KT * 128 + k4 * 32, 16, 1024, tc::kLayoutSW128), id_s,
-                                 kk > 0 ? 1u : 0u);
-                }
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_bf16(tmem + C::s_col(u), qd + (kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2,
+                                 kd + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2, id_s, kk > 0 ? 1u : 0u);
                 tc::commit(&B.s_full[u]);
                 if (pair || u == 1) tc::commit(&B.kv_empty[st]);
-                return true;
-            };
-            bool ok = wait(&B.q_full, 0, 5, false);
-            tc::fence_after();
-            for (int u = 0; ok && u < 2; ++u)
-                if (count_of(u) > 0) ok = product_s(u, 0);
-            const int steps = count_of(0);       // the longer stream
-            for (int i = 0; ok && i < steps; ++i) {
-                for (int u = 0; ok && u < 2; ++u) {
-                    if (i >= count_of(u)) continue;
-                    const int k = 2 * tile_of(u, i) + 1, st = k % C::kStages;
-                    ok = wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 6, false) &&
-                         wait(&B.p_full[u], (uint32_t)i, 7, false);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t vs = smem_u32(ring + st * C::kTile);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = all_wait(&B.q_full, 0, 5);
+        tc::fence_after();
+        for (int u = 0; ok && u < 2; ++u)
+            if (count_of(u) > 0) ok = product_s(u, 0);
+        const int steps = count_of(0);           // the longer stream
+        for (int i = 0; ok && i < steps; ++i) {
+            for (int u = 0; ok && u < 2; ++u) {
+                if (i >= count_of(u)) continue;
+                const int k = 2 * tile_of(u, i) + 1, st = k % C::kStages;
+                ok = all_wait(&B.kv_full[st], (uint32_t)(k / C::kStages), 6) && all_wait(&B.p_full[u], (uint32_t)i, 7);
+                if (!ok) break;
+                tc::fence_after();
+                const uint64_t vd = v_desc + (uint64_t)(st * (C::kTile >> 4));
+                if (tc::elect_one()) {
 #pragma unroll
                     for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
                             tc::mma_f16_ts(tmem + C::o_col(u),
                                            tmem + (uint32_t)(C::s_col(u) + part * C::kPCols + kk * 8),
-                                           tc::smem_desc(vs + kk * 16 * 128, KT * 128, 1024, tc::kLayoutSW128), id_o,
-                                           (i > 0 || kk > 0 || part > 0) ? 1u : 0u);
+                                           vd + kk * (16 * 128 >> 4), id_o, (i > 0 || kk > 0 || part > 0) ? 1u : 0u);
                     if (i == count_of(u) - 1) tc::commit(&B.o_full[u]);
                     if (pair || u == 1) tc::commit(&B.kv_empty[st]);
-                    if (i + 1 < count_of(u)) ok = product_s(u, i + 1);
                 }
-            }
-            if (!ok) {                           // let what was issued finish
-                tc::commit(&B.drain);
-                tc::mbar_wait_bounded(&B.drain, 0, kPfWaitNs, K_CACHE_PREFIX, 8);
+                __syncwarp();
+                if (i + 1 < count_of(u)) ok = product_s(u, i + 1);
             }
         }
-        __syncwarp();
+        if (!ok) {                               // let what was issued finish
+            if (tc::elect_one()) tc::commit(&B.drain);
+            __syncwarp();
+            tc::mbar_wait_bounded(&B.drain, 0, kPfWaitNs, K_CACHE_PREFIX, 8);
+        }
     } else {
         // ---- softmax: stream u, row r of its tile
         const int u = warp >> 2, r = (warp & 3) * 32 + lane;

@@ -60,6 +60,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
+// True in one lane of a converged warp, the same one each time.  Unlike lane == 0 the
+// compiler knows that a single thread runs the branch: descriptors stay in uniform
+// registers, and issuing a tcgen05.mma costs a few cycles instead of about a hundred.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 // Arrive on an mbarrier once every tcgen05.mma issued so far by this thread completes.
 __device__ __forceinline__ void commit(uint64_t *mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(

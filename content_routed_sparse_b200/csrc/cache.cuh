@@ -82,6 +82,9 @@ inline int cache_sms() {
     return sms;
 }
 
+constexpr int kCaRows = 16;            // query rows of an item (M of mma.sync)
+constexpr int kCaKeys = 64;            // keys per tile
+
 // What the attention kernels and the merge of their partial results are given.
 struct CaArgs {
     CacheDev c;
@@ -91,18 +94,218 @@ struct CaArgs {
     int M;             // query rows of one (sequence, KV head): n_tok * G
     int RT;            // row tiles of an own item
     int prefix_len;
-    int PT;            // key tiles of a prefix item of cache_attn_kernel (0: none)
+    int PT;            // key tiles of a prefix item (0: the prefix has a pass of its own)
     int PRT;           // its row tiles, over n_seq * M rows
-    int grid;          // CTAs of cache_attn_kernel
+    int grid;          // CTAs that share the tile sequence
     int tc_splits;     // key splits of cache_prefix_kernel (0: not launched)
     int tc_tiles;      // its row tiles per KV head, kPfRows rows each
     float scale_log2, decay;
     float *part_o, *part_ml;       // pieces: [piece][16][D], [piece][16][2] (m in log2 units, l)
     float *tc_o, *tc_ml;           // [split][KV head][n_seq * M][D], [..][2]
+    int *cum;                      // [n_seq + 1] units of the sequences before each
     float *logits;                 // [sequence][KV head][M][ls] log2-scaled, or null
     int ls;
     void *O;
     float *lse, *mass_out;
 };
+
+
+// The work of the batch in units.  An item of T key tiles counts T + kItemCost units, the
+// first of them for its start and end (query rows, first maximum, result), which cost
+// about what a tile does; the items' units follow one another and CTA c of the grid has
+// [c w, (c + 1) w).  Tile t of an item that starts at unit x is unit x + kItemCost + t.
+constexpr int kItemCost = 1;
+
+__device__ __forceinline__ int ca_units(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
+__device__ __forceinline__ long long ca_prefix_units(const CaArgs &a) {
+    return (long long)a.c.n_kv * a.PRT * ca_units(a.PT);
+}
+__device__ __forceinline__ long long ca_share(const CaArgs &a, long long W) {
+    return W > a.grid ? (W + a.grid - 1) / a.grid : 1;
+}
+
+// What a CTA keeps of the sequences' lengths, in shared memory: where its share starts, and
+// the slots in use before and with the new tokens of the kLensKept sequences from there
+// (later ones are read again where they are needed).
+constexpr int kLensKept = 64;
+struct CaLens {
+    long long units;               // of the whole batch (prefix items aside: per KV head and row tile)
+    int first;                     // the sequence that the CTA's share starts in
+    int before;                    // units of the sequences before it
+    int scan[8];
+    int len[kLensKept], tot[kLensKept];
+};
+__device__ __forceinline__ void ca_lens_of(const CaArgs &a, const CaLens &L, int s, int &len, int &total) {
+    const int k = s - L.first;
+    if ((unsigned)k < (unsigned)kLensKept) {
+        len = L.len[k];
+        total = L.tot[k];
+    } else {
+        len = cache_len(a.c, s);
+        total = len + cache_new(a.c, a.n_new, a.n_tok, s, len);
+    }
+}
+// key tiles of a sequence's own items (none without a token to ask)
+__device__ __forceinline__ int ca_tiles(int len, int total) {
+    return total > len ? (total + kCaKeys - 1) / kCaKeys : 0;
+}
+__device__ __forceinline__ int ca_tiles_of(const CaArgs &a, const CaLens &L, int s) {
+    int len, total;
+    ca_lens_of(a, L, s, len, total);
+    return ca_tiles(len, total);
+}
+
+// Fills it (one block; barriers inside).  CTA 0 leaves the units of the sequences before
+// each one in a.cum for the merge.
+template <int THREADS> __device__ __forceinline__ void ca_cumulate(const CaArgs &a, CaLens &L) {
+    const int n = a.c.n_seq, per = (n + THREADS - 1) / THREADS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
+    auto units_of = [&](int s) {
+        const int len = cache_len(a.c, s);
+        return ca_units(ca_tiles(len, len + cache_new(a.c, a.n_new, a.n_tok, s, len)));
+    };
+    int sum = 0;
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) sum += units_of(s);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) L.scan[warp] = inc;
+    if (tid == 0) {
+        L.first = n;
+        L.before = 0;
+    }
+    __syncthreads();
+    int base = inc - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += L.scan[w];
+        all += L.scan[w];
+    }
+    const long long P = ca_prefix_units(a), K = (long long)a.c.n_kv * a.RT;
+    const long long n0 = max(0LL, blockIdx.x * ca_share(a, P + all * K) - P);      // of the own items
+    if (tid == 0) L.units = all;
+    if (base * K <= n0 && n0 < (long long)(base + sum) * K) {
+        int b = base;
+        for (int s = s0; s < s1; ++s) {
+            const int u = units_of(s);
+            if (n0 < (long long)(b + u) * K) {
+                L.first = s;
+                L.before = b;
+                break;
+            }
+            b += u;
+        }
+    }
+    if (blockIdx.x == 0) {
+        if (tid == 0) a.cum[0] = 0;
+        int b = base;
+        for (int s = s0; s < s1; ++s) {
+            b += units_of(s);
+            a.cum[s + 1] = b;
+        }
+    }
+    __syncthreads();
+    const int s = L.first + tid;
+    if (tid < kLensKept && s < n) {
+        const int len = cache_len(a.c, s);
+        L.len[tid] = len;
+        L.tot[tid] = len + cache_new(a.c, a.n_new, a.n_tok, s, len);
+    }
+    __syncthreads();
+}
+
+// A tile in the sequence of a CTA's tiles.
+struct CaCursor {
+    bool prefix;
+    int s, h, rt;                  // own: sequence, KV head, row tile; prefix: h, rt
+    int t, T;                      // tile of the item, tiles of the item
+    long long unit, stop;          // the tile's unit; the CTA's share ends before unit stop
+    __device__ __forceinline__ bool more() const { return unit < stop; }
+    // the last tile of the item, or of the CTA's share of it
+    __device__ __forceinline__ bool ends() const { return t == T - 1 || unit == stop - 1; }
+};
+
+__device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const CaLens &L) {
+    CaCursor u;
+    const long long P = ca_prefix_units(a), K = (long long)a.c.n_kv * a.RT;
+    const long long W = P + L.units * K, w = ca_share(a, W);
+    const long long n0 = blockIdx.x * w;
+    u.stop = min(W, n0 + w);
+    u.unit = n0;
+    u.prefix = n0 < P;
+    u.s = u.h = u.rt = u.t = 0;
+    u.T = 1;
+    if (n0 >= W) return u;
+    long long r;
+    if (u.prefix) {
+        const int U = ca_units(a.PT), x = (int)(n0 / U);
+        u.h = x / a.PRT;
+        u.rt = x - u.h * a.PRT;
+        u.T = a.PT;
+        r = n0 - (long long)x * U;
+    } else {
+        u.s = L.first;
+        u.T = ca_tiles_of(a, L, u.s);
+        const int U = ca_units(u.T);
+        r = n0 - P - (long long)L.before * K;
+        const int y = (int)(r / U);
+        r -= (long long)y * U;
+        u.h = y / a.RT;
+        u.rt = y - u.h * a.RT;
+    }
+    if (r < kItemCost) u.unit += kItemCost - r;
+    else u.t = (int)r - kItemCost;
+    return u;
+}
+// the next tile (its fields mean nothing once more() is false)
+__device__ __forceinline__ void ca_advance(const CaArgs &a, const CaLens &L, CaCursor &u) {
+    ++u.unit;
+    if (++u.t < u.T) return;
+    u.t = 0;
+    u.unit += kItemCost;
+    if (++u.rt < (u.prefix ? a.PRT : a.RT)) return;
+    u.rt = 0;
+    if (++u.h < a.c.n_kv) return;
+    u.h = 0;
+    if (u.prefix) {
+        u.prefix = false;
+        u.s = 0;
+    } else {
+        ++u.s;
+    }
+    for (u.T = 0; u.s < a.c.n_seq && u.T == 0; ++u.s) u.T = ca_tiles_of(a, L, u.s);
+    if (u.T > 0) --u.s;                          // the first sequence from there with a tile
+    else u.T = 1;
+}
+__device__ __forceinline__ long long ca_item(const CaArgs &a, const CaCursor &u) {
+    return u.prefix ? (long long)u.h * a.PRT + u.rt
+                    : (long long)a.c.n_kv * a.PRT + ((long long)u.s * a.c.n_kv + u.h) * a.RT + u.rt;
+}
+
+// Row r of an item's tile of query rows: where it lies (null: no such row), and how many
+// keys it sees (slots or prefix keys below lim).
+__device__ __forceinline__ const __nv_bfloat16 *ca_query(const CaArgs &a, const CaLens &L, const CaCursor &u, int r,
+                                                         int *lim = nullptr) {
+    int R = u.rt * kCaRows + r, s = u.s;
+    if (lim) *lim = 0;
+    if (u.prefix) {
+        if (R >= a.c.n_seq * a.M) return nullptr;
+        s = R / a.M;
+        R -= s * a.M;
+    } else if (R >= a.M) {
+        return nullptr;
+    }
+    int len, total;
+    ca_lens_of(a, L, s, len, total);
+    const int i = R / a.G, g = R - i * a.G;
+    if (i >= total - len) return nullptr;
+    if (lim) *lim = u.prefix ? a.prefix_len : len + i + 1;
+    return a.Q + (((size_t)s * a.n_tok + i) * a.n_q + u.h * a.G + g) * a.c.D;
+}
 
 }  // namespace crs

@@ -3,164 +3,37 @@
 //
 // The work is a list of items: (KV head, tile of query rows) over the prefix, where
 // the rows are the whole batch's queries of that head, and (sequence, KV head, tile
-// of its query rows) over its own slots.  An item's keys are cut into tiles of 64.
-// All tiles of all items form one sequence of W tiles, and CTA c of a fixed grid
-// (as many as fit on the GPU) takes tiles [c w, (c + 1) w), w = ceil(W / grid): the
-// lengths live on the device, and ragged batches stay balanced without the host
-// knowing them.  A CTA's share of an item is a piece with its own softmax state
-// (m, l, unnormalised O); piece number = CTA + item, which is unique because one of
-// the two grows from piece to piece.  cache_merge_kernel joins the pieces, divides,
-// and turns the logits kept in the workspace into accumulated weights.
+// of its query rows) over its own slots.  An item's keys are cut into tiles; the tiles
+// of all items form one sequence, of which every CTA of a fixed grid (as many as fit on
+// the GPU) takes an equal share: the lengths live on the device, and ragged batches stay
+// balanced without the host knowing them.  A CTA's share of an item is a piece with its
+// own softmax state (m, l, unnormalised O); piece number = CTA + item, which is unique
+// because one of the two grows from piece to piece.  cache_merge_kernel joins the
+// pieces, divides, and turns the logits kept in the workspace into accumulated weights.
+//
+// The prefix of a larger batch has a pass of its own (cache_prefix.cu).
 #include <math.h>
 
 #include "cache.cuh"
 
 namespace crs {
 
-constexpr int kCaKeys = 64;            // keys per tile
 constexpr int kCaWarps = 4;            // each takes 16 keys of a tile
 constexpr int kCaThreads = kCaWarps * 32;
-constexpr int kCaStages = 3;           // K/V tiles in the ring
-constexpr int kCaRows = 16;            // query rows of an item (M of mma.sync)
+constexpr int kCaStages = 2;           // K/V tiles in the ring
 constexpr int kCaRing = kCaStages + 1; // tiles whose row lists are kept
 constexpr int kCaTcRows = 16;          // rows per KV head above which the prefix goes to the tensor cores
 constexpr int kMgThreads = 256;
-constexpr int kMgSlots = 512;          // slots whose mass one CTA updates
-
-// key tiles of a sequence's own items (none without a new token to ask)
-__device__ __forceinline__ int ca_tiles(const CaArgs &a, int s) {
-    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
-    return n > 0 ? (len + n + kCaKeys - 1) / kCaKeys : 0;
-}
-__device__ __forceinline__ long long ca_prefix_tiles(const CaArgs &a) {
-    return (long long)a.c.n_kv * a.PRT * a.PT;
-}
-__device__ __forceinline__ long long ca_share(const CaArgs &a, long long W) {
-    return W > a.grid ? (W + a.grid - 1) / a.grid : 1;
-}
-
-// Position in the tile sequence.
-struct CaCursor {
-    bool prefix;
-    int s, h, rt;      // own: sequence, KV head, row tile; prefix: h, rt
-    int t, T;          // tile of the item, tiles of the item
-};
-
-__device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const int *cum, long long n) {
-    CaCursor u;
-    const long long P = ca_prefix_tiles(a);
-    u.prefix = n < P;
-    if (u.prefix) {
-        const int x = (int)(n / a.PT);
-        u.s = 0;
-        u.h = x / a.PRT;
-        u.rt = x - u.h * a.PRT;
-        u.t = (int)(n - (long long)x * a.PT);
-        u.T = a.PT;
-        return u;
-    }
-    n -= P;
-    const long long K = (long long)a.c.n_kv * a.RT;
-    int lo = 0, hi = a.c.n_seq;                 // cum[lo] K <= n < cum[hi] K
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)cum[mid] * K <= n) lo = mid;
-        else hi = mid;
-    }
-    const long long r = n - (long long)cum[lo] * K;
-    u.s = lo;
-    u.T = cum[lo + 1] - cum[lo];
-    const int y = (int)(r / u.T);
-    u.t = (int)(r - (long long)y * u.T);
-    u.h = y / a.RT;
-    u.rt = y - u.h * a.RT;
-    return u;
-}
-// the next tile; past the last one the cursor must not be used
-__device__ __forceinline__ void ca_advance(const CaArgs &a, const int *cum, CaCursor &u) {
-    if (++u.t < u.T) return;
-    u.t = 0;
-    if (++u.rt < (u.prefix ? a.PRT : a.RT)) return;
-    u.rt = 0;
-    if (++u.h < a.c.n_kv) return;
-    u.h = 0;
-    if (u.prefix) {
-        u.prefix = false;
-        u.s = 0;
-    } else {
-        ++u.s;
-    }
-    while (u.s < a.c.n_seq && cum[u.s + 1] == cum[u.s]) ++u.s;
-    u.T = u.s < a.c.n_seq ? cum[u.s + 1] - cum[u.s] : 1;
-}
-__device__ __forceinline__ long long ca_item(const CaArgs &a, const CaCursor &u) {
-    return u.prefix ? (long long)u.h * a.PRT + u.rt
-                    : (long long)a.c.n_kv * a.PRT + ((long long)u.s * a.c.n_kv + u.h) * a.RT + u.rt;
-}
-
-// cum[s] = tiles of the sequences before s, s = 0..n_seq (one block; barriers inside)
-__device__ __forceinline__ void ca_cumulate(const CaArgs &a, int *cum, int *scratch) {
-    const int n = a.c.n_seq, per = (n + kCaThreads - 1) / kCaThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
-    int sum = 0;
-    for (int s = s0; s < s1; ++s) {
-        const int T = ca_tiles(a, s);
-        cum[s + 1] = T;
-        sum += T;
-    }
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += scratch[w];
-    for (int s = s0; s < s1; ++s) {
-        base += cum[s + 1];
-        cum[s + 1] = base;
-    }
-    if (tid == 0) cum[0] = 0;
-    __syncthreads();
-}
-
-// The query row R of an item: its token's index, whether it exists, where it lies.
-struct CaRow {
-    int lim;                       // keys it sees (slots or prefix keys below lim)
-    const __nv_bfloat16 *q;        // null: no such row
-};
-__device__ __forceinline__ CaRow ca_row(const CaArgs &a, const CaCursor &u, int r) {
-    CaRow w;
-    w.lim = 0;
-    w.q = nullptr;
-    int R = u.rt * kCaRows + r, s = u.s;
-    if (u.prefix) {
-        if (R >= a.c.n_seq * a.M) return w;
-        s = R / a.M;
-        R -= s * a.M;
-    } else if (R >= a.M) {
-        return w;
-    }
-    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
-    const int i = R / a.G, g = R - i * a.G;
-    if (i >= n) return w;
-    w.lim = u.prefix ? a.prefix_len : len + i + 1;
-    w.q = a.Q + (((size_t)s * a.n_tok + i) * a.n_q + u.h * a.G + g) * a.c.D;
-    return w;
-}
 
 template <int D> constexpr int ca_tile_bytes() { return kCaKeys * D * 2; }
 template <int D> constexpr int ca_scratch_bytes() { return D / 8 * 32 * 16; }
-template <int D> constexpr int ca_smem_bytes(int n_seq) {
+template <int D> constexpr int ca_smem_bytes() {
     return 2 * kCaStages * ca_tile_bytes<D>() + ca_scratch_bytes<D>() + kCaRing * kCaKeys * 4 + kCaRing * 2 * 8 +
-           kCaWarps * 16 * 2 * 4 + 64 + (n_seq + 1) * 4;
+           kCaWarps * 16 * 2 * 4;
 }
 
-// CTAs per SM: as many as the shared memory (108 and 55 KB) and the registers hold
-template <int D> constexpr int ca_per_sm() { return D == 128 ? 2 : 4; }
+// CTAs per SM: as many as the shared memory (76 and 38 KB) and the registers hold
+template <int D> constexpr int ca_per_sm() { return D == 128 ? 3 : 5; }
 
 // byte offset of 16-byte chunk c of row r of a tile (rows of 2 D bytes, chunks XORed by row)
 template <int D> __device__ __forceinline__ int ca_off(int r, int c) { return r * (D * 2) + ((c ^ (r & 7)) << 4); }
@@ -168,6 +41,7 @@ template <int D> __device__ __forceinline__ int ca_off(int r, int c) { return r 
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(CaArgs a) {
     extern __shared__ __align__(128) unsigned char ca_smem[];
+    static_assert(ca_per_sm<D>() * (ca_smem_bytes<D>() + (int)sizeof(CaLens) + 1024 + 64) <= 233472, "CTAs per SM");
     constexpr int kTile = ca_tile_bytes<D>(), kChunks = D / 8;
     unsigned char *sK = ca_smem;                                       // [stages][64 rows][2 D bytes]
     unsigned char *sV = sK + kCaStages * kTile;
@@ -176,25 +50,20 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     int *sRow = reinterpret_cast<int *>(sBase + kCaRing * 2);          // [ring][64]: token row, -1: none
     float *sM = reinterpret_cast<float *>(sRow + kCaRing * kCaKeys);   // [warps][16]
     float *sL = sM + kCaWarps * 16;
-    int *sScan = reinterpret_cast<int *>(sL + kCaWarps * 16);
-    int *cum = sScan + 16;                                             // [n_seq + 1]
+    __shared__ CaLens lens;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g_row = lane >> 2, tig = lane & 3;
 
-    ca_cumulate(a, cum, sScan);
-    const long long W = ca_prefix_tiles(a) + (long long)cum[a.c.n_seq] * a.c.n_kv * a.RT;
-    const long long w = ca_share(a, W);
-    const long long n0 = blockIdx.x * w;
-    if (n0 >= W) return;
-    const int n_tiles = (int)min(w, W - n0);
+    ca_cumulate<kCaThreads>(a, lens);
+    CaCursor ahead = ca_seek(a, lens);           // next tile whose rows are listed
+    CaCursor cur = ahead;                        // tile being consumed
+    if (!cur.more()) return;
+    int listed = 0;
 
     const size_t tok_stride = (size_t)a.c.n_kv * D;
-    CaCursor ahead = ca_seek(a, cum, n0);        // next tile whose rows are listed
-    CaCursor cur = ahead;                        // tile being consumed
-
     // rows of the ahead tile into ring slot i % kCaRing
     auto list_tile = [&](int i) {
-        if (i >= n_tiles) return;
+        if (!ahead.more()) return;
         const int slot = i % kCaRing;
         if (tid < kCaKeys) {
             const int j = ahead.t * kCaKeys + tid;
@@ -202,8 +71,9 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
             if (ahead.prefix) {
                 if (j < a.prefix_len) row = j;
             } else {
-                const int len = cache_len(a.c, ahead.s);
-                if (j < len + cache_new(a.c, a.n_new, a.n_tok, ahead.s, len)) row = cache_row(a.c, ahead.s, j);
+                int len, total;
+                ca_lens_of(a, lens, ahead.s, len, total);
+                if (j < total) row = cache_row(a.c, ahead.s, j);
             }
             sRow[slot * kCaKeys + tid] = row;
             if (tid == 0) {
@@ -211,11 +81,12 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
                 sBase[slot * 2 + 1] = (ahead.prefix ? a.pv : a.c.v) + ahead.h * D;
             }
         }
-        ca_advance(a, cum, ahead);
+        ca_advance(a, lens, ahead);
+        ++listed;
     };
     // 16-byte copies of tile i's K and V rows (one commit group, empty past the last tile)
     auto load_tile = [&](int i) {
-        if (i < n_tiles) {
+        if (i < listed) {
             const int slot = i % kCaRing, buf = i % kCaStages;
             const __nv_bfloat16 *Kb = sBase[slot * 2], *Vb = sBase[slot * 2 + 1];
 #pragma unroll
@@ -243,21 +114,20 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     float *log_lo = nullptr, *log_hi = nullptr;
     bool fresh = true;                           // the next tile starts a piece
 
-    for (int i = 0; i < n_tiles; ++i) {
+    for (int i = 0; cur.more(); ++i) {
         const int buf = i % kCaStages, slot = i % kCaRing;
         if (fresh) {                             // query fragments straight from global memory
             fresh = false;
-            const CaRow lo = ca_row(a, cur, g_row), hi = ca_row(a, cur, g_row + 8);
-            lim_lo = lo.lim;
-            lim_hi = hi.lim;
+            const __nv_bfloat16 *q_lo = ca_query(a, lens, cur, g_row, &lim_lo);
+            const __nv_bfloat16 *q_hi = ca_query(a, lens, cur, g_row + 8, &lim_hi);
             lim_max = __reduce_max_sync(0xffffffffu, max(lim_lo, lim_hi));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int col = kk * 16 + e * 8 + tig * 2;
-                    qf[kk][2 * e] = lo.q ? *reinterpret_cast<const uint32_t *>(lo.q + col) : 0u;
-                    qf[kk][2 * e + 1] = hi.q ? *reinterpret_cast<const uint32_t *>(hi.q + col) : 0u;
+                    qf[kk][2 * e] = q_lo ? *reinterpret_cast<const uint32_t *>(q_lo + col) : 0u;
+                    qf[kk][2 * e + 1] = q_hi ? *reinterpret_cast<const uint32_t *>(q_hi + col) : 0u;
                 }
             }
 #pragma unroll
@@ -375,7 +245,7 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
         }
 
         // ---- end of the piece: the warps' states are joined in warp order through 16 D floats
-        if (cur.t == cur.T - 1 || i == n_tiles - 1) {
+        if (cur.ends()) {
             fresh = true;
             l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
             l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
@@ -438,7 +308,7 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
             }
             __syncthreads();                     // sM, sL and sAcc are reused
         }
-        ca_advance(a, cum, cur);
+        ca_advance(a, lens, cur);
     }
     cp_async_wait<0>();
 }
@@ -452,9 +322,9 @@ struct MgRow {
     int h;
     long long r_tc;            // row of the tensor-core prefix pass
 };
-__device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, int before, int T, long long W) {
+__device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, int before, int T, long long w) {
     MgRow m;
-    const long long w = ca_share(a, W), P = ca_prefix_tiles(a);
+    const long long P = ca_prefix_units(a);
     m.n_own = m.n_pre = 0;
     m.own0 = m.pre0 = 0;
     m.h = h;
@@ -462,7 +332,8 @@ __device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, in
     m.r_own = R - rt * kCaRows;
     if (T > 0) {
         const long long x = ((long long)s * a.c.n_kv + h) * a.RT + rt;
-        const long long first = P + (long long)before * a.c.n_kv * a.RT + ((long long)h * a.RT + rt) * T;
+        const long long first = P + (long long)before * a.c.n_kv * a.RT +
+                                ((long long)h * a.RT + rt) * (T + kItemCost) + kItemCost;
         const long long c0 = first / w, c1 = (first + T - 1) / w;
         m.own0 = c0 + (long long)a.c.n_kv * a.PRT + x;
         m.n_own = (int)(c1 - c0 + 1);
@@ -472,7 +343,7 @@ __device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, in
     if (a.PT > 0) {
         const int prt = (int)(Rg / kCaRows);
         m.r_pre = (int)(Rg - (long long)prt * kCaRows);
-        const long long x = (long long)h * a.PRT + prt, first = x * a.PT;
+        const long long x = (long long)h * a.PRT + prt, first = x * ca_units(a.PT) + kItemCost;
         const long long c0 = first / w, c1 = (first + a.PT - 1) / w;
         m.pre0 = c0 + x;
         m.n_pre = (int)(c1 - c0 + 1);
@@ -512,72 +383,55 @@ __device__ __forceinline__ void mg_stat(const CaArgs &a, const MgRow &m, int lan
     L = warp_sum(l);
 }
 
-// tiles of the sequences before s, and of all (one block)
-__device__ __forceinline__ void mg_before(const CaArgs &a, int s, int &before, int &all) {
-    __shared__ int red[2][kMgThreads / 32];
-    int b = 0, t = 0;
-    for (int q = threadIdx.x; q < a.c.n_seq; q += kMgThreads) {
-        const int T = ca_tiles(a, q);
-        t += T;
-        if (q < s) b += T;
-    }
-    b = warp_sum_int(b);
-    t = warp_sum_int(t);
-    if ((threadIdx.x & 31) == 0) {
-        red[0][threadIdx.x >> 5] = b;
-        red[1][threadIdx.x >> 5] = t;
-    }
-    __syncthreads();
-    before = all = 0;
-#pragma unroll
-    for (int v = 0; v < kMgThreads / 32; ++v) {
-        before += red[0][v];
-        all += red[1][v];
-    }
-}
-
-// CTAs [0, n_o) join pieces: WPR warps per row, 8 / WPR rows of one (sequence, KV head)
-// each; the CTAs after them update kMgSlots slots' mass each.
-template <int D, int WPR, typename OutT>
-__global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int n_o, int row_groups, int chunks) {
-    constexpr int kRowsPer = 8 / WPR, kE = D / 32;
-    extern __shared__ float mg_smem[];           // mass CTAs: [M] lse in log2 units
+// CTA (sequence, KV head, chunk): joins the pieces of rows chunk, chunk + chunks, ... and
+// updates every chunks-th run of 512 slots' mass.  A row with few peers in its CTA has
+// several warps, each with a part of its pieces.
+template <int D, typename OutT>
+__global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int chunks) {
+    constexpr int kE = D / 32;
+    extern __shared__ float2 mg_stats[];         // [M] (m, l)
     __shared__ float red[8][D];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool joins = (int)blockIdx.x < n_o;
-    const int idx = joins ? blockIdx.x : blockIdx.x - n_o;
-    const int per = joins ? row_groups : chunks;
-    const int sh = idx / per, part = idx - sh * per;
+    const int sh = blockIdx.x / chunks, chunk = blockIdx.x - sh * chunks;
     const int s = sh / a.c.n_kv, h = sh - s * a.c.n_kv;
+    const int before = a.cum[s], after = a.cum[s + 1], all = a.cum[a.c.n_seq];
     const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
-    const int total = len + n;
-    if (!joins && part * kMgSlots >= total) return;
-    int before, all;
-    mg_before(a, s, before, all);
-    const long long W = ca_prefix_tiles(a) + (long long)all * a.c.n_kv * a.RT;
-    const int T = n > 0 ? (total + kCaKeys - 1) / kCaKeys : 0;
+    const int total = len + n, rows = n * a.G;
+    const int T = after > before ? after - before - kItemCost : 0;
+    const long long w = ca_share(a, ca_prefix_units(a) + (long long)all * a.c.n_kv * a.RT);
 
-    if (joins) {
-        const int R = part * kRowsPer + warp / WPR, sub = warp % WPR;
-        const int i = R / a.G;
-        const bool exists = R < a.M;
-        const bool live = exists && i < n;
+    const bool mass = a.logits && chunk * 2 * kMgThreads < total;
+    const int step = mass ? 1 : chunks;          // the rows whose statistics are needed
+    for (int R = (mass ? 0 : chunk) + warp * step; R < rows; R += 8 * step) {
+        const MgRow m = mg_row(a, s, h, R, before, T, w);
+        float Mx, L;
+        mg_stat(a, m, lane, Mx, L);
+        if (lane == 0) mg_stats[R] = make_float2(Mx, L);
+    }
+    __syncthreads();
+
+    const int mine = (a.M - chunk + chunks - 1) / chunks;      // rows of this CTA
+    const int wpr = mine >= 5 ? 1 : mine >= 3 ? 2 : mine == 2 ? 4 : 8;
+    const int sub = warp % wpr;
+    for (int q0 = 0; q0 < mine; q0 += 8 / wpr) {
+        const int q = q0 + warp / wpr, R = chunk + q * chunks;
+        const bool live = q < mine && R < rows;
         float acc[kE];
 #pragma unroll
         for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
-        float Mx = -INFINITY, L = 0.0f;
+        float2 st = make_float2(-INFINITY, 0.0f);
         if (live) {
-            const MgRow m = mg_row(a, s, h, R, before, T, W);
-            mg_stat(a, m, lane, Mx, L);
+            st = mg_stats[R];
+            const MgRow m = mg_row(a, s, h, R, before, T, w);
             const int np = m.n_own + m.n_pre;
-            if (Mx != -INFINITY) {
+            if (st.x != -INFINITY) {
 #pragma unroll 4
-                for (int p = sub; p < np; p += WPR) {
+                for (int p = sub; p < np; p += wpr) {
                     const float *o, *ml;
                     const size_t k = mg_piece(a, m, p, o, ml);
                     const float pm = ml[k * 2];
                     if (pm == -INFINITY) continue;
-                    const float f = exp2f(pm - Mx);
+                    const float f = exp2f(pm - st.x);
                     const float *src = o + k * D + lane * kE;
                     if constexpr (kE == 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(src);
@@ -589,67 +443,72 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int n
                 }
             }
         }
-        if constexpr (WPR > 1) {
+        if (wpr > 1) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
             __syncthreads();
             if (sub == 0) {
-#pragma unroll
-                for (int v = 1; v < WPR; ++v)
+                for (int v = 1; v < wpr; ++v)
 #pragma unroll
                     for (int e = 0; e < kE; ++e) acc[e] += red[warp + v][lane * kE + e];
             }
+            __syncthreads();
         }
-        if (exists && sub == 0) {
-            const int g = R - i * a.G;
+        if (q < mine && sub == 0) {
+            const int i = R / a.G, g = R - i * a.G;
             const size_t row = ((size_t)s * a.n_tok + i) * a.n_q + h * a.G + g;
             OutT *dst = static_cast<OutT *>(a.O) + row * D + lane * kE;
-            const float f = L == 0.0f ? 0.0f : 1.0f / L;
             // nothing seen: zeros; a NaN or infinite sum passes through
+            const float L = st.y, f = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
             for (int e = 0; e < kE; e += 2) {
                 const float x = L == 0.0f ? 0.0f : acc[e] * f, y = L == 0.0f ? 0.0f : acc[e + 1] * f;
                 if constexpr (sizeof(OutT) == 4) *reinterpret_cast<float2 *>(dst + e) = make_float2(x, y);
                 else *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(x, y);
             }
-            if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (Mx + log2f(L)) * 0.6931471805599453f;
+            if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (st.x + log2f(L)) * 0.6931471805599453f;
         }
-        return;
     }
+    if (!mass) return;
 
-    // ---- mass: sum over the rows of 2^(logit - lse)
-    for (int R = warp; R < a.M; R += 8) {
-        float v = INFINITY;                      // a row that does not exist or sees nothing adds 0
-        if (R / a.G < n) {
-            const MgRow m = mg_row(a, s, h, R, before, T, W);
-            float Mx, L;
-            mg_stat(a, m, lane, Mx, L);
-            if (L != 0.0f) v = Mx + log2f(L);
+    // ---- mass: sum over the rows of 2^(logit - lse); a row that sees nothing adds 0
+    float *z = reinterpret_cast<float *>(mg_stats);
+    __syncthreads();
+    float zr[1024 / kMgThreads];
+#pragma unroll
+    for (int q = 0; q < 1024 / kMgThreads; ++q) {
+        const int R = tid + q * kMgThreads;
+        if (R < rows) {
+            const float2 st = mg_stats[R];
+            zr[q] = st.y != 0.0f ? st.x + log2f(st.y) : INFINITY;
         }
-        if (lane == 0) mg_smem[R] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 1024 / kMgThreads; ++q) {
+        const int R = tid + q * kMgThreads;
+        if (R < rows) z[R] = zr[q];
     }
     __syncthreads();
     const float *lg = a.logits + (size_t)sh * a.M * a.ls;
-    const int j = part * kMgSlots + tid * 2;
-    if (j >= total) return;
-    float x = 0.0f, y = 0.0f;
-    const int rows = n * a.G;
+    for (int j = (chunk * kMgThreads + tid) * 2; j < total; j += chunks * 2 * kMgThreads) {
+        float x = 0.0f, y = 0.0f;
 #pragma unroll 4
-    for (int R = 0; R < rows; ++R) {
-        const float2 v = *reinterpret_cast<const float2 *>(lg + (size_t)R * a.ls + j);
-        const float z = mg_smem[R];
-        x += exp2f(v.x - z);
-        y += exp2f(v.y - z);
+        for (int R = 0; R < rows; ++R) {
+            const float2 v = *reinterpret_cast<const float2 *>(lg + (size_t)R * a.ls + j);
+            x += exp2f(v.x - z[R]);
+            y += exp2f(v.y - z[R]);
+        }
+        const size_t at = (size_t)sh * a.c.cap + j;
+        a.mass_out[at] = a.decay * a.c.mass[at] + x;
+        if (j + 1 < total) a.mass_out[at + 1] = a.decay * a.c.mass[at + 1] + y;
     }
-    const size_t at = (size_t)sh * a.c.cap + j;
-    a.mass_out[at] = a.decay * a.c.mass[at] + x;
-    if (j + 1 < total) a.mass_out[at + 1] = a.decay * a.c.mass[at + 1] + y;
 }
 
 // ----------------------------------------------------------------------------- host --
 struct CaPlan {
     int grid, PT, PRT, RT, M, tc_splits, tc_tiles;
-    size_t part_o, part_ml, tc_o, tc_ml, logits, total;   // workspace offsets
+    size_t part_o, part_ml, tc_o, tc_ml, cum, logits, total;   // workspace offsets
     int ls;
 };
 
@@ -694,6 +553,8 @@ static CaPlan ca_plan(const crs_cache_attn_params *p) {
     at += up(parts * D * 4);
     q.tc_ml = at;
     at += up(parts * 2 * 4);
+    q.cum = at;
+    at += up(((size_t)p->c.n_seq + 1) * 4);
     q.ls = ceil_div(p->c.cap, kCaKeys) * kCaKeys;
     q.logits = at;
     if (p->want_mass) at += up((size_t)p->c.n_seq * p->c.n_kv * q.M * q.ls * 4);
@@ -702,7 +563,7 @@ static CaPlan ca_plan(const crs_cache_attn_params *p) {
 }
 
 template <int D, bool SPLIT> int ca_launch(const CaArgs &a, cudaStream_t s) {
-    const int smem = ca_smem_bytes<D>(a.c.n_seq);
+    const int smem = ca_smem_bytes<D>();
     CRS_TRY_CUDA(
         cudaFuncSetAttribute(cache_attn_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope _ps(K_CACHE_ATTN, s);
@@ -711,18 +572,15 @@ template <int D, bool SPLIT> int ca_launch(const CaArgs &a, cudaStream_t s) {
     return CRS_OK;
 }
 
-template <int D, typename OutT> int mg_launch(const CaArgs &a, int want_mass, cudaStream_t s) {
-    const long long rows = (long long)a.c.n_seq * a.c.n_kv * a.M;
-    // one warp per row when the rows fill the GPU, else eight share a row's pieces
-    const bool wide = rows < (long long)cache_sms() * 16;
-    const int groups = wide ? a.M : ceil_div(a.M, 8);
-    const long long n_o = (long long)a.c.n_seq * a.c.n_kv * groups;
-    const int chunks = want_mass ? ceil_div(a.c.cap, kMgSlots) : 0;
-    const long long ctas = n_o + (long long)a.c.n_seq * a.c.n_kv * chunks;
-    if (ctas > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
+template <int D, typename OutT> int mg_launch(const CaArgs &a, cudaStream_t s) {
+    const long long sh = (long long)a.c.n_seq * a.c.n_kv;
+    // about six CTAs per SM, as far as there are rows and slots to spread
+    const long long want = ceil_div_ll((long long)cache_sms() * 6, sh);
+    const long long most = max(a.M, a.logits ? ceil_div(a.c.cap, 2 * kMgThreads) : 1);
+    const int chunks = (int)max(1LL, min(want, most));
+    if (sh * chunks > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
     ProfScope _ps(K_CACHE_MERGE, s);
-    if (wide) cache_merge_kernel<D, 8, OutT><<<(unsigned)ctas, kMgThreads, a.M * 4, s>>>(a, (int)n_o, groups, chunks);
-    else cache_merge_kernel<D, 1, OutT><<<(unsigned)ctas, kMgThreads, a.M * 4, s>>>(a, (int)n_o, groups, chunks);
+    cache_merge_kernel<D, OutT><<<(unsigned)(sh * chunks), kMgThreads, a.M * 8, s>>>(a, chunks);
     CRS_CHECK_LAUNCH();
     return CRS_OK;
 }
@@ -774,6 +632,7 @@ extern "C" int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_st
     a.part_ml = reinterpret_cast<float *>(w + q.part_ml);
     a.tc_o = reinterpret_cast<float *>(w + q.tc_o);
     a.tc_ml = reinterpret_cast<float *>(w + q.tc_ml);
+    a.cum = reinterpret_cast<int *>(w + q.cum);
     a.logits = p->want_mass ? reinterpret_cast<float *>(w + q.logits) : nullptr;
     a.ls = q.ls;
     a.O = O;
@@ -788,6 +647,6 @@ extern "C" int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_st
     if (p->c.D == 128) e = f32 ? ca_launch<128, true>(a, s) : ca_launch<128, false>(a, s);
     else e = f32 ? ca_launch<64, true>(a, s) : ca_launch<64, false>(a, s);
     if (e) return e;
-    if (p->c.D == 128) return f32 ? mg_launch<128, float>(a, p->want_mass, s) : mg_launch<128, __nv_bfloat16>(a, p->want_mass, s);
-    return f32 ? mg_launch<64, float>(a, p->want_mass, s) : mg_launch<64, __nv_bfloat16>(a, p->want_mass, s);
+    if (p->c.D == 128) return f32 ? mg_launch<128, float>(a, s) : mg_launch<128, __nv_bfloat16>(a, s);
+    return f32 ? mg_launch<64, float>(a, s) : mg_launch<64, __nv_bfloat16>(a, s);
 }

@@ -85,6 +85,28 @@ inline int cache_sms() {
 constexpr int kCaRows = 16;            // query rows of an item (M of mma.sync)
 constexpr int kCaKeys = 64;            // keys per tile
 
+// Programmatic dependent launch: the next kernel of the chain may start once every CTA of
+// this one has said so, and waits for the end of this one where it needs its results.
+// Without the launch attribute both do nothing.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem, cudaStream_t s, bool chained,
+                           Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // What the attention kernels and the merge of their partial results are given.
 struct CaArgs {
     CacheDev c;
@@ -126,12 +148,13 @@ __device__ __forceinline__ long long ca_share(const CaArgs &a, long long W) {
 
 // What a CTA keeps of the sequences' lengths, in shared memory: where its share starts, and
 // the slots in use before and with the new tokens of the kLensKept sequences from there
-// (later ones are read again where they are needed).
-constexpr int kLensKept = 64;
+// (all of a batch that has no more; others are read again where they are needed).
+constexpr int kLensKept = 128;
 struct CaLens {
     long long units;               // of the whole batch (prefix items aside: per KV head and row tile)
-    int first;                     // the sequence that the CTA's share starts in
+    int start;                     // the sequence that the CTA's share of the own items starts in
     int before;                    // units of the sequences before it
+    int first;                     // the first one kept
     int scan[8];
     int len[kLensKept], tot[kLensKept];
 };
@@ -165,9 +188,20 @@ template <int THREADS> __device__ __forceinline__ void ca_cumulate(const CaArgs 
         const int len = cache_len(a.c, s);
         return ca_units(ca_tiles(len, len + cache_new(a.c, a.n_new, a.n_tok, s, len)));
     };
+    static_assert(THREADS >= kLensKept, "a thread per kept sequence");
+    const bool all_kept = n <= kLensKept;
     int sum = 0;
+    if (all_kept) {
+        if (tid < n) {
+            const int len = cache_len(a.c, tid), total = len + cache_new(a.c, a.n_new, a.n_tok, tid, len);
+            L.len[tid] = len;
+            L.tot[tid] = total;
+            sum = ca_units(ca_tiles(len, total));
+        }
+    } else {
 #pragma unroll 4
-    for (int s = s0; s < s1; ++s) sum += units_of(s);
+        for (int s = s0; s < s1; ++s) sum += units_of(s);
+    }
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +210,8 @@ template <int THREADS> __device__ __forceinline__ void ca_cumulate(const CaArgs 
     }
     if (lane == 31) L.scan[warp] = inc;
     if (tid == 0) {
-        L.first = n;
+        L.start = n;
+        L.first = 0;
         L.before = 0;
     }
     __syncthreads();
@@ -189,12 +224,23 @@ template <int THREADS> __device__ __forceinline__ void ca_cumulate(const CaArgs 
     const long long P = ca_prefix_units(a), K = (long long)a.c.n_kv * a.RT;
     const long long n0 = max(0LL, blockIdx.x * ca_share(a, P + all * K) - P);      // of the own items
     if (tid == 0) L.units = all;
-    if (base * K <= n0 && n0 < (long long)(base + sum) * K) {
+    const bool here = base * K <= n0 && n0 < (long long)(base + sum) * K;
+    if (all_kept) {
+        if (here) {
+            L.start = tid;
+            L.before = base;
+        }
+        if (blockIdx.x == 0 && tid < n) a.cum[tid + 1] = base + sum;
+        if (blockIdx.x == 0 && tid == 0) a.cum[0] = 0;
+        __syncthreads();
+        return;
+    }
+    if (here) {
         int b = base;
         for (int s = s0; s < s1; ++s) {
             const int u = units_of(s);
             if (n0 < (long long)(b + u) * K) {
-                L.first = s;
+                L.start = L.first = s;
                 L.before = b;
                 break;
             }
@@ -249,7 +295,7 @@ __device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const CaLens &L) {
         u.T = a.PT;
         r = n0 - (long long)x * U;
     } else {
-        u.s = L.first;
+        u.s = L.start;
         u.T = ca_tiles_of(a, L, u.s);
         const int U = ca_units(u.T);
         r = n0 - P - (long long)L.before * K;

@@ -54,10 +54,14 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g_row = lane >> 2, tig = lane & 3;
 
+    dependents_may_start();
     ca_cumulate<kCaThreads>(a, lens);
     CaCursor ahead = ca_seek(a, lens);           // next tile whose rows are listed
     CaCursor cur = ahead;                        // tile being consumed
-    if (!cur.more()) return;
+    if (!cur.more()) {
+        wait_for_previous();
+        return;
+    }
     int listed = 0;
 
     const size_t tok_stride = (size_t)a.c.n_kv * D;
@@ -311,6 +315,7 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
         ca_advance(a, lens, cur);
     }
     cp_async_wait<0>();
+    wait_for_previous();                         // the merge waits for this kernel, and so for the prefix pass too
 }
 
 // --------------------------------------------------------------------------- merge --
@@ -353,34 +358,34 @@ __device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, in
     }
     return m;
 }
-// index of piece p of the row: its (m, l) pair and its D floats, in the arrays ml and o
-__device__ __forceinline__ size_t mg_piece(const CaArgs &a, const MgRow &m, int p, const float *&o, const float *&ml) {
-    o = a.part_o;
-    ml = a.part_ml;
+// Piece p of the row: index of its (m, l) pair, and of its D floats, in the arrays of the
+// slots' pass (tc false) or of the prefix pass.
+__device__ __forceinline__ size_t mg_piece(const CaArgs &a, const MgRow &m, int p, bool &tc) {
+    tc = false;
     if (p < m.n_own) return (size_t)(m.own0 + p) * kCaRows + m.r_own;
     if (a.PT > 0) return (size_t)(m.pre0 + p - m.n_own) * kCaRows + m.r_pre;
-    o = a.tc_o;
-    ml = a.tc_ml;
+    tc = true;
     return ((size_t)(p - m.n_own) * a.c.n_kv + m.h) * ((size_t)a.c.n_seq * a.M) + (size_t)m.r_tc;
 }
 
-// largest m and total l of the row's pieces (one warp; -inf and 0 when there is nothing)
-__device__ __forceinline__ void mg_stat(const CaArgs &a, const MgRow &m, int lane, float &Mx, float &L) {
+// Largest m and total l of the row's pieces (one warp; -inf and 0 when there is nothing).
+__device__ __forceinline__ float2 mg_stat(const CaArgs &a, const MgRow &m, int lane) {
     const int n = m.n_own + m.n_pre;
-    const float *o, *ml;
-    float mx = -INFINITY;
+    float mx = -INFINITY, l = 0.0f;
     for (int p = lane; p < n; p += 32) {
-        const size_t k = mg_piece(a, m, p, o, ml);
-        mx = fmaxf(mx, ml[k * 2]);
+        bool tc;
+        const size_t k = mg_piece(a, m, p, tc);
+        const float2 v = *reinterpret_cast<const float2 *>((tc ? a.tc_ml : a.part_ml) + k * 2);
+        const float mn = fmax_nan(mx, v.x);
+        if (mn == -INFINITY) continue;
+        l = l * exp2f(mx - mn) + v.y * exp2f(v.x - mn);
+        mx = mn;
     }
-    Mx = warp_max(mx);
-    float l = 0.0f;
-    for (int p = lane; p < n; p += 32) {
-        const size_t k = mg_piece(a, m, p, o, ml);
-        const float2 v = *reinterpret_cast<const float2 *>(ml + k * 2);
-        if (v.x != -INFINITY) l += v.y * exp2f(v.x - Mx);
-    }
-    L = warp_sum(l);
+    float Mx = mx;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) Mx = fmax_nan(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
+    l = warp_sum(mx == -INFINITY ? 0.0f : l * exp2f(mx - Mx));
+    return make_float2(Mx, l);
 }
 
 // CTA (sequence, KV head, chunk): joins the pieces of rows chunk, chunk + chunks, ... and
@@ -394,6 +399,7 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sh = blockIdx.x / chunks, chunk = blockIdx.x - sh * chunks;
     const int s = sh / a.c.n_kv, h = sh - s * a.c.n_kv;
+    wait_for_previous();
     const int before = a.cum[s], after = a.cum[s + 1], all = a.cum[a.c.n_seq];
     const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
     const int total = len + n, rows = n * a.G;
@@ -404,9 +410,8 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int c
     const int step = mass ? 1 : chunks;          // the rows whose statistics are needed
     for (int R = (mass ? 0 : chunk) + warp * step; R < rows; R += 8 * step) {
         const MgRow m = mg_row(a, s, h, R, before, T, w);
-        float Mx, L;
-        mg_stat(a, m, lane, Mx, L);
-        if (lane == 0) mg_stats[R] = make_float2(Mx, L);
+        const float2 st = mg_stat(a, m, lane);
+        if (lane == 0) mg_stats[R] = st;
     }
     __syncthreads();
 
@@ -425,20 +430,35 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int c
             const MgRow m = mg_row(a, s, h, R, before, T, w);
             const int np = m.n_own + m.n_pre;
             if (st.x != -INFINITY) {
-#pragma unroll 4
-                for (int p = sub; p < np; p += wpr) {
-                    const float *o, *ml;
-                    const size_t k = mg_piece(a, m, p, o, ml);
-                    const float pm = ml[k * 2];
-                    if (pm == -INFINITY) continue;
-                    const float f = exp2f(pm - st.x);
-                    const float *src = o + k * D + lane * kE;
-                    if constexpr (kE == 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(src);
-                        acc[0] += f * v.x; acc[1] += f * v.y; acc[2] += f * v.z; acc[3] += f * v.w;
-                    } else {
-                        const float2 v = *reinterpret_cast<const float2 *>(src);
-                        acc[0] += f * v.x; acc[1] += f * v.y;
+                // lane q knows the address and the weight of the warp's q-th piece
+                for (int p0 = sub; p0 < np; p0 += 32 * wpr) {
+                    const int mine_p = p0 + lane * wpr, count = min(32, (np - p0 + wpr - 1) / wpr);
+                    const float *src = nullptr;
+                    float f = 0.0f;
+                    if (mine_p < np) {
+                        bool tc;
+                        const size_t k = mg_piece(a, m, mine_p, tc);
+                        const float pm = (tc ? a.tc_ml : a.part_ml)[k * 2];
+                        src = (tc ? a.tc_o : a.part_o) + k * D;
+                        f = pm == -INFINITY ? 0.0f : exp2f(pm - st.x);
+                    }
+#pragma unroll 8
+                    for (int q = 0; q < count; ++q) {
+                        const float *from = reinterpret_cast<const float *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), q));
+                        const float fq = __shfl_sync(0xffffffffu, f, q);
+                        // a piece whose rows all saw nothing may hold anything: weight 0, not added
+                        if constexpr (kE == 4) {
+                            const float4 v = *reinterpret_cast<const float4 *>(from + lane * 4);
+                            if (fq != 0.0f) {
+                                acc[0] += fq * v.x; acc[1] += fq * v.y; acc[2] += fq * v.z; acc[3] += fq * v.w;
+                            }
+                        } else {
+                            const float2 v = *reinterpret_cast<const float2 *>(from + lane * 2);
+                            if (fq != 0.0f) {
+                                acc[0] += fq * v.x; acc[1] += fq * v.y;
+                            }
+                        }
                     }
                 }
             }
@@ -567,21 +587,20 @@ template <int D, bool SPLIT> int ca_launch(const CaArgs &a, cudaStream_t s) {
     CRS_TRY_CUDA(
         cudaFuncSetAttribute(cache_attn_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope _ps(K_CACHE_ATTN, s);
-    cache_attn_kernel<D, SPLIT><<<a.grid, kCaThreads, smem, s>>>(a);
-    CRS_CHECK_LAUNCH();
+    CRS_TRY_CUDA(launch_chained(cache_attn_kernel<D, SPLIT>, (unsigned)a.grid, kCaThreads, smem, s, a.tc_splits > 0, a));
     return CRS_OK;
 }
 
 template <int D, typename OutT> int mg_launch(const CaArgs &a, cudaStream_t s) {
     const long long sh = (long long)a.c.n_seq * a.c.n_kv;
-    // about six CTAs per SM, as far as there are rows and slots to spread
-    const long long want = ceil_div_ll((long long)cache_sms() * 6, sh);
+    // one wave (four CTAs fit on an SM), as far as there are rows and slots to spread
+    const long long want = (long long)cache_sms() * 4 / sh;
     const long long most = max(a.M, a.logits ? ceil_div(a.c.cap, 2 * kMgThreads) : 1);
     const int chunks = (int)max(1LL, min(want, most));
     if (sh * chunks > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
     ProfScope _ps(K_CACHE_MERGE, s);
-    cache_merge_kernel<D, OutT><<<(unsigned)(sh * chunks), kMgThreads, a.M * 8, s>>>(a, chunks);
-    CRS_CHECK_LAUNCH();
+    CRS_TRY_CUDA(launch_chained(cache_merge_kernel<D, OutT>, (unsigned)(sh * chunks), kMgThreads, (size_t)a.M * 8, s, true,
+                                a, chunks));
     return CRS_OK;
 }
 

@@ -106,6 +106,7 @@ cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __
     unsigned char *ring = sQ + 2 * C::kQ;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);      // uniform for the compiler too
+    dependents_may_start();
 
     const int mt = blockIdx.x % a.tc_tiles, rest = blockIdx.x / a.tc_tiles;
     const int split = rest % a.tc_splits, h = rest / a.tc_splits;
@@ -150,6 +151,8 @@ cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __
     if (warp == 16) {
         // ---- K_0, V_0, K_1, V_1, ... through the ring
         if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&tm_k) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&tm_v) : "memory");
             int issued = 0;
             for (; issued < 2 * n; ++issued) {
                 const int st = issued % C::kStages, use = issued / C::kStages;

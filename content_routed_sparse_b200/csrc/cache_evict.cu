@@ -2,10 +2,10 @@
 // the others from the paged cache, sm_100a.
 //
 // Selection: one CTA per (sequence, KV head) holds the slots' order-preserving 32-bit
-// keys in registers, consecutive slots per thread.  The keep-th largest key is found
-// bit by bit from the top, one CTA-wide count per bit, without atomics; a scan of the
-// counts above and at it places the kept slots in ascending order, ties to the lower
-// slot.  Longer caches than the registers hold re-read the keys from memory: four
+// keys in registers, consecutive slots per warp.  The keep-th largest key is found from
+// the top, two bits per CTA-wide count, until few keys are left between, which one warp
+// finishes; a scan of the warps' counts above and at it, and ballots, place the kept
+// slots in ascending order, ties to the lower slot.  Longer caches than the registers hold re-read the keys from memory: four
 // passes with 256-bin histograms, then the same placement.
 //
 // Eviction: nothing depends on the order of a head's slots, so only the kept slots
@@ -52,11 +52,28 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *warp_sums, ui
     return inc - v + __shfl_sync(0xffffffffu, winc - w, warp);
 }
 
+constexpr int kMassList = 256;                   // keys that one warp searches
+
+// Warp w holds the 32 KPT slots from w 32 KPT, slot i 32 + lane of them in lane's key[i]:
+// loads and the kept slots' stores are contiguous, and ballots rank the slots in order.
+// CTA-wide sums of two values per thread, as cta_count
+__device__ __forceinline__ int2 cta_count2(int x, int y, int &ph) {
+    __shared__ int2 cbuf[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wx = __reduce_add_sync(0xffffffffu, x), wy = __reduce_add_sync(0xffffffffu, y);
+    if (lane == 0) cbuf[ph][warp] = make_int2(wx, wy);
+    __syncthreads();
+    const int2 v = lane < (int)(blockDim.x >> 5) ? cbuf[ph][lane] : make_int2(0, 0);
+    ph ^= 1;
+    return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
+}
+
 template <int THREADS, int KPT>
 __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
-    __shared__ uint32_t sums[32];
+    __shared__ uint32_t sums[32], list[kMassList], found;
+    __shared__ int listed;
     const int sh = blockIdx.x, s = sh / a.n_kv, h = sh - s * a.n_kv;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int len = min(max(a.seq_len[s], 0), a.cap), k = min(a.keep, len);
     int32_t *out = a.idx + (size_t)sh * a.keep;
     if (h == 0 && tid == 0) a.count[s] = k;
@@ -68,24 +85,82 @@ __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
     const float *mass = a.mass + (size_t)sh * a.cap;
     const int32_t *pos = a.pos ? a.pos + (size_t)sh * a.cap : nullptr;
     const int recent = a.pos ? a.next_pos[s] - a.window : 0;
-    const int j0 = tid * KPT;
+    const int j0 = (tid >> 5) * (32 * KPT) + lane;
     uint32_t key[KPT];
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-        const int j = j0 + i;
-        key[i] = j < len ? sel_key(mass[j], pos ? pos[j] : 0, pos != nullptr, a.sink_end, recent, nan) : 0u;
+        const int j = j0 + i * 32;
+        key[i] = j < len ? __float_as_uint(mass[j]) : 0u;
+    }
+    // 16 positions at a time: all 2 KPT loads in flight would need the registers twice
+#pragma unroll
+    for (int i0 = 0; i0 < KPT; i0 += 16) {
+        int p[KPT < 16 ? KPT : 16];
+#pragma unroll
+        for (int i = 0; i < (KPT < 16 ? KPT : 16); ++i) {
+            const int j = j0 + (i0 + i) * 32;
+            p[i] = pos && j < len ? pos[j] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < (KPT < 16 ? KPT : 16); ++i) {
+            const int j = j0 + (i0 + i) * 32;
+            key[i0 + i] = j < len ? sel_key(__uint_as_float(key[i0 + i]), p[i], pos != nullptr, a.sink_end, recent, nan) : 0u;
+        }
     }
     if (nan) raise_error(CRS_DEVERR_NONFINITE);
-    // the largest threshold that at least k keys reach
+    // The largest threshold T that at least k keys reach, two bits at a time: n_lo keys reach
+    // T, n_hi reach T + 2^b.  Once few keys lie between, one warp finishes among them.
     uint32_t T = 0u;
-    int ph = 0;
-    for (int b = 31; b >= 0; --b) {
-        const uint32_t cand = T | (1u << b);
-        int n = 0;
+    int n_lo = THREADS * KPT, n_hi = 0, b = 32, ph = 0;
+    while (b > 0 && n_lo - n_hi > kMassList) {
+        b -= 2;
+        int c12 = 0, c3 = 0;
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) n += key[i] >= cand;
-        if (cta_count(n, ph) >= k) T = cand;
+        for (int i = 0; i < KPT; ++i) {
+            c12 += key[i] >= T + (1u << b);
+            c12 += key[i] >= T + (2u << b) ? 0x10000 : 0;
+            c3 += key[i] >= T + (3u << b);
+        }
+        const int2 n = cta_count2(c12, c3, ph);
+        const int n1 = n.x & 0xffff, n2 = n.x >> 16, n3 = n.y;
+        if (n3 >= k) { T += 3u << b; n_lo = n3; }
+        else if (n2 >= k) { T += 2u << b; n_lo = n2; n_hi = n3; }
+        else if (n1 >= k) { T += 1u << b; n_lo = n1; n_hi = n2; }
+        else n_hi = n1;
+    }
+    if (b > 0) {
+        if (tid == 0) listed = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const bool in = (key[i] - T) >> b == 0u;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (m == 0u) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&listed, __popc(m));
+            at = __shfl_sync(0xffffffffu, at, 0);
+            if (in) list[at + __popc(m & ((1u << lane) - 1u))] = key[i];   // the order does not matter
+        }
+        __syncthreads();
+        if (tid < 32) {
+            uint32_t mine[kMassList / 32];
+#pragma unroll
+            for (int i = 0; i < kMassList / 32; ++i) {
+                const int e = i * 32 + lane;
+                mine[i] = e < listed ? list[e] : 0u;
+            }
+            for (int q = b - 1; q >= 0; --q) {
+                const uint32_t cand = T | (1u << q);
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kMassList / 32; ++i) n += mine[i] >= cand;
+                if (n_hi + __reduce_add_sync(0xffffffffu, n) >= k) T = cand;
+            }
+            if (lane == 0) found = T;
+        }
+        __syncthreads();
+        T = found;
     }
     // slots past len have key 0 and follow every slot of the sequence: they lose every tie
     uint32_t gt = 0, eq = 0;
@@ -94,16 +169,21 @@ __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
         gt += key[i] > T;
         eq += key[i] == T;
     }
+    // the warp's slots above the threshold and at it, and those of the warps before it
+    const uint32_t own = __reduce_add_sync(0xffffffffu, gt | (eq << 16));
     uint32_t total;
-    const uint32_t before = cta_scan(gt | (eq << 16), sums, total);
+    const uint32_t before = __shfl_sync(0xffffffffu, cta_scan(lane == 0 ? own : 0u, sums, total), 0);
     const uint32_t need = (uint32_t)k - (total & 0xffffu);
-    uint32_t eb = before >> 16;
-    uint32_t at = (before & 0xffffu) + min(eb, need);
+    uint32_t eb = before >> 16, at = (before & 0xffffu) + min(eb, need);
+    const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-        bool take = key[i] > T;
-        if (key[i] == T) take = eb++ < need;
-        if (take) out[at++] = j0 + i;
+        const uint32_t e = __ballot_sync(0xffffffffu, key[i] == T);
+        const bool take = key[i] > T || (key[i] == T && eb + __popc(e & lower) < need);
+        const uint32_t t = __ballot_sync(0xffffffffu, take);
+        if (take) out[at + __popc(t & lower)] = j0 + i * 32;
+        eb += __popc(e);
+        at += __popc(t);
     }
 }
 

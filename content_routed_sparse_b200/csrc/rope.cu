@@ -1,15 +1,15 @@
 // Rotary positions and the append of rotated rows to the paged cache, sm_100a.
 //
-// The rotation moves every element once: it is bound by memory.  A thread owns one
-// vector of pairs of one token, forms their cosines and sines once, and applies them
-// to several heads (they do not depend on the head), so the angle's cost is shared;
-// with few tokens the heads are spread over threads instead.
+// The rotation moves every element once: it is bound by memory, as long as the angles'
+// cost is shared.  A CTA takes a few tokens, forms their cosines and sines once in shared
+// memory, and walks the tokens' heads in memory order.
 #include "cache.cuh"
 
 namespace crs {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;          // heads whose loads are in flight together
+constexpr int kRopeBatch = 2;          // vectors of pairs whose loads are in flight together, per thread
+constexpr int kRopePerSm = 4;          // CTAs per SM
 
 template <int BYTES> struct VecOf;
 template <> struct VecOf<16> { using type = uint4; };
@@ -66,102 +66,170 @@ template <int V, bool INTER> struct RopeUnit {
     }
 };
 
+// The angles of a CTA's tokens, in shared memory: (cos, sin) of two pairs to 16 bytes (of
+// one to 8 when V is 1), the pieces of a unit's V pairs apart, so that the threads of
+// neighbouring units read neighbouring 16 bytes.
+template <int V> struct RopeTable {
+    static constexpr int kPieces = V > 1 ? V / 2 : 1, kPairs = V > 1 ? 2 : 1;
+    float *base;
+    int tokens, n_rot;
+    __device__ __forceinline__ float *at(int t, int u, int piece) const {
+        return base + ((piece * tokens + t) * n_rot + u) * (2 * kPairs);
+    }
+    // pair j of token t
+    __device__ __forceinline__ float2 *pair(int t, int j) const {
+        const int u = j / V, i = j - u * V;
+        return reinterpret_cast<float2 *>(at(t, u, i / kPairs)) + i % kPairs;
+    }
+    __device__ __forceinline__ void load(int t, int u, float2 (&cs)[V]) const {
+        if constexpr (V == 1) {
+            cs[0] = *reinterpret_cast<const float2 *>(at(t, u, 0));
+        } else {
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const float4 w = *reinterpret_cast<const float4 *>(at(t, u, p));
+                cs[2 * p] = make_float2(w.x, w.y);
+                cs[2 * p + 1] = make_float2(w.z, w.w);
+            }
+        }
+    }
+};
+
 // (a, b) of V pairs turned in place; interleaved: the pairs are neighbours in a, then b.
 template <typename T, int V, bool INTER>
-__device__ __forceinline__ void rope_turn(Pack<T, V> &a, Pack<T, V> &b, const float (&c)[V], const float (&s)[V]) {
-    if constexpr (INTER) {
+__device__ __forceinline__ void rope_turn(Pack<T, V> &a, Pack<T, V> &b, const float2 (&cs)[V]) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i) {
+        T *pa, *pb;
+        if constexpr (INTER && V > 1) {
             Pack<T, V> &w = 2 * i < V ? a : b;               // pair i: elements 2i, 2i + 1 of (a, b)
-            const int at = (2 * i) % V;
-            if constexpr (V == 1) {
-                const float x = to_f32(a.e[0]), y = to_f32(b.e[0]);
-                a.e[0] = from_f32<T>(x * c[0] - y * s[0]);
-                b.e[0] = from_f32<T>(y * c[0] + x * s[0]);
-            } else {
-                const float x = to_f32(w.e[at]), y = to_f32(w.e[at + 1]);
-                w.e[at] = from_f32<T>(x * c[i] - y * s[i]);
-                w.e[at + 1] = from_f32<T>(y * c[i] + x * s[i]);
-            }
+            pa = &w.e[(2 * i) % V];
+            pb = &w.e[(2 * i) % V + 1];
+        } else {
+            pa = &a.e[i];
+            pb = &b.e[i];
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float x = to_f32(a.e[i]), y = to_f32(b.e[i]);
-            a.e[i] = from_f32<T>(x * c[i] - y * s[i]);
-            b.e[i] = from_f32<T>(y * c[i] + x * s[i]);
-        }
+        const float x = to_f32(*pa), y = to_f32(*pb);
+        *pa = from_f32<T>(x * cs[i].x - y * cs[i].y);
+        *pb = from_f32<T>(y * cs[i].x + x * cs[i].y);
     }
 }
+
+// n / d for n < 2^31 by one multiplication (d >= 1; the quotient is exact: Granlund and
+// Montgomery's round-up method, with the shift and the factor found on the host)
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi((uint32_t)n, mul) >> shift); }
+};
+inline FastDiv fast_div(int d) {
+    FastDiv f;
+    f.d = (uint32_t)d;
+    if (d == 1) {                                // n * (2^32 - 1) / 2^32 would be n - 1
+        f.mul = 0;
+        f.shift = 0;
+        return f;
+    }
+    int l = 0;
+    while ((1LL << l) < d) ++l;                  // 2^(l-1) < d <= 2^l
+    // m = ceil(2^(31 + l) / d) < 2^32; n m / 2^(31 + l) is exact for n < 2^31
+    f.mul = (uint32_t)(((1ULL << (31 + l)) + (uint32_t)d - 1) / (uint32_t)d);
+    f.shift = (uint32_t)(l - 1);
+    return f;
+}
+__device__ __forceinline__ int fd_quot(const FastDiv &f, int n) { return f.d == 1 ? n : f.of(n); }
+
+// What a CTA does: it turns `tokens` consecutive tokens, heads [h0, h1) of them.  The
+// angles are formed once, in shared memory; the vectors are then walked in memory order
+// (unit, head, token), kRopeBatch loads in flight per thread.
+constexpr int kRopeMost = 8 * kRopeThreads;      // vectors of pairs of a CTA
+constexpr int kRopeSmem = 16384;                 // bytes of (cos, sin) pairs a CTA may hold
 
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 rope_kernel(const T *x, T *y, const int32_t *__restrict__ pos, const double *__restrict__ inv_freq, int n_tok, int heads,
-            int per_group, int D, int rot_begin, int rot_dim, long long xs, long long ys, float mscale, int inverse,
-            int units) {
-    const int n_rot = rot_dim / (2 * V);
-    const long long e = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-    const int t = (int)(e / units);
-    if (t >= n_tok) return;
-    const int u = (int)(e - (long long)t * units);
-    const RopeUnit<V, INTER> at(u, n_rot, rot_begin, rot_dim);
-    float c[V], s[V];
-    if (at.rot) {
-        const int p = pos[t];
-#pragma unroll
-        for (int i = 0; i < V; ++i) rope_angle(p, inv_freq[u * V + i], mscale, inverse != 0, c[i], s[i]);
+            int tokens, int per_group, int D, int rot_begin, int rot_dim, long long xs, long long ys, float mscale,
+            int inverse, FastDiv units, FastDiv group) {
+    extern __shared__ __align__(16) float rope_cs[];
+    const int half = rot_dim / 2, n_rot = half / V;
+    const RopeTable<V> table{rope_cs, tokens, n_rot};
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, n_tok - t0);
+    const int h0 = blockIdx.y * per_group, nh = min(per_group, heads - h0);
+    for (int e = threadIdx.x; e < nt * half; e += kRopeThreads) {
+        const int t = e / half, j = e - t * half;
+        float2 *to = table.pair(t, j);
+        rope_angle(pos[t0 + t], inv_freq[j], mscale, inverse != 0, to->x, to->y);
     }
-    const int h0 = blockIdx.y * per_group, h1 = min(heads, h0 + per_group);
-    for (int h = h0; h < h1; h += kRopeBatch) {
+    __syncthreads();
+    const int items = nt * per_group * (int)units.d;
+    for (int e0 = threadIdx.x; e0 < items; e0 += kRopeThreads * kRopeBatch) {
         Pack<T, V> a[kRopeBatch], b[kRopeBatch];
+        T *dst[kRopeBatch];
+        int tok[kRopeBatch], unit[kRopeBatch], off[kRopeBatch];      // (unit -1: copied), b's offset from a
 #pragma unroll
         for (int q = 0; q < kRopeBatch; ++q) {
-            if (h + q < h1) {
-                const T *row = x + t * xs + (long long)(h + q) * D;
-                a[q].load(row + at.a);
-                if (at.rot) b[q].load(row + at.b);
-            }
+            const int e = e0 + q * kRopeThreads;
+            dst[q] = nullptr;
+            if (e >= items) continue;
+            const int th = fd_quot(units, e), u = e - th * (int)units.d;
+            const int t = fd_quot(group, th), h = th - t * (int)group.d;
+            if (h >= nh) continue;
+            const RopeUnit<V, INTER> at(u, n_rot, rot_begin, rot_dim);
+            const T *row = x + (t0 + t) * xs + (long long)(h0 + h) * D;
+            a[q].load(row + at.a);
+            if (at.rot) b[q].load(row + at.b);
+            dst[q] = y + (t0 + t) * ys + (long long)(h0 + h) * D + at.a;
+            off[q] = at.b - at.a;
+            tok[q] = t;
+            unit[q] = at.rot ? u : -1;
         }
 #pragma unroll
         for (int q = 0; q < kRopeBatch; ++q) {
-            if (h + q < h1) {
-                T *row = y + t * ys + (long long)(h + q) * D;
-                if (at.rot) {
-                    rope_turn<T, V, INTER>(a[q], b[q], c, s);
-                    b[q].store(row + at.b);
-                }
-                a[q].store(row + at.a);
+            if (!dst[q]) continue;
+            if (unit[q] >= 0) {
+                float2 cs[V];
+                table.load(tok[q], unit[q], cs);
+                rope_turn<T, V, INTER>(a[q], b[q], cs);
+                b[q].store(dst[q] + off[q]);
             }
+            a[q].store(dst[q]);
         }
     }
 }
 
-// Heads per thread: all of them while the tokens alone fill the GPU (the angles are
-// shared), fewer when there are few tokens.
-inline int rope_groups(long long items, int heads, int sms) {
-    const long long want = (long long)sms * 1536;
-    long long g = items > 0 ? (want + items - 1) / items : 1;
-    if (g < 1) g = 1;
-    if (g > heads) g = heads;
-    return (int)g;
+// Tokens and head groups of a CTA: up to eight vectors of pairs per thread while that leaves
+// some eight CTAs per SM (the angles are shared by the heads of a CTA), less work per CTA
+// in smaller calls.
+inline void rope_shape(long long n_tok, int heads, int units, int half, int sms, int &tokens, int &groups) {
+    const long long vectors = n_tok * heads * units;
+    long long per = vectors / ((long long)sms * 8);              // vectors per CTA
+    per = per < kRopeThreads ? kRopeThreads : per > kRopeMost ? kRopeMost : per;
+    tokens = (int)(per / ((long long)heads * units));
+    groups = 1;
+    if (tokens < 1) {
+        tokens = 1;
+        groups = (int)(((long long)heads * units + per - 1) / per);
+        if (groups > heads) groups = heads;
+    }
+    const int most = half > 0 ? kRopeSmem / (half * 8) : tokens;
+    if (tokens > most && most >= 1) tokens = most;
+    if (tokens > n_tok) tokens = (int)n_tok;
 }
 
 template <typename T, int V>
 int rope_launch(const crs_rope_params *p, int n_tok, int heads, const void *x, long long xs, const int32_t *pos,
                 const double *inv_freq, void *y, long long ys, cudaStream_t s) {
-    const int units = p->rot_dim / (2 * V) + (p->D - p->rot_dim) / V;
-    const long long items = (long long)n_tok * units;
-    const int per_group = ceil_div(heads, rope_groups(items, heads, cache_sms()));
-    const dim3 grid((unsigned)ceil_div_ll(items, kRopeThreads), (unsigned)ceil_div(heads, per_group));
+    const int half = p->rot_dim / 2, units = half / V + (p->D - p->rot_dim) / V;
+    int tokens, groups;
+    rope_shape(n_tok, heads, units, half, cache_sms(), tokens, groups);
+    const int per_group = ceil_div(heads, groups);
+    const dim3 grid((unsigned)ceil_div(n_tok, tokens), (unsigned)ceil_div(heads, per_group));
+    const size_t smem = (size_t)tokens * half * 8;
+    const FastDiv du = fast_div(units), dg = fast_div(per_group);
     ProfScope _ps(K_ROPE, s);
-    if (p->interleaved)
-        rope_kernel<T, V, true><<<grid, kRopeThreads, 0, s>>>(
-            static_cast<const T *>(x), static_cast<T *>(y), pos, inv_freq, n_tok, heads, per_group, p->D, p->rot_begin,
-            p->rot_dim, xs, ys, p->mscale, p->inverse, units);
-    else
-        rope_kernel<T, V, false><<<grid, kRopeThreads, 0, s>>>(
-            static_cast<const T *>(x), static_cast<T *>(y), pos, inv_freq, n_tok, heads, per_group, p->D, p->rot_begin,
-            p->rot_dim, xs, ys, p->mscale, p->inverse, units);
+    auto kern = p->interleaved ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
+    kern<<<grid, kRopeThreads, smem, s>>>(static_cast<const T *>(x), static_cast<T *>(y), pos, inv_freq, n_tok, heads,
+                                          tokens, per_group, p->D, p->rot_begin, p->rot_dim, xs, ys, p->mscale,
+                                          p->inverse, du, dg);
     return cudaGetLastError() == cudaSuccess ? CRS_OK : CRS_ERR_CUDA;
 }
 
@@ -181,78 +249,97 @@ struct AppendArgs {
     long long ks, vs, qs;
     const double *inv_freq;
     const int32_t *n_new;
-    int n_tok, n_q, rot_begin, rot_dim, units, per_group, inverse;
+    int n_tok, n_q, rot_begin, rot_dim, tokens, per_group, inverse;
     float mscale;
+    FastDiv units, group;
 };
+constexpr int kApTokens = 64;                    // tokens of a CTA at most
 
-// Heads are numbered k, v, q: a thread takes one vector of pairs of one token through
-// its group of them.
+// As rope_kernel, over the heads k, v, q of the batch's tokens; where a token's rows go is
+// found once per token.
 template <bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) cache_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopePerSm) cache_append_kernel(AppendArgs a) {
     constexpr int V = 8;
     using P = Pack<__nv_bfloat16, V>;
-    const long long e = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-    const long long tok = e / a.units;
-    if (tok >= (long long)a.c.n_seq * a.n_tok) return;
-    const int u = (int)(e - tok * a.units);
-    const int s = (int)(tok / a.n_tok), i = (int)(tok - (long long)s * a.n_tok);
-    const int n_kv = a.c.n_kv, D = a.c.D;
-    const RopeUnit<V, INTER> at(u, a.rot_dim / (2 * V), a.rot_begin, a.rot_dim);
-    const int hh0 = blockIdx.y * a.per_group, hh1 = min(2 * n_kv + a.n_q, hh0 + a.per_group);
-
-    const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
-    const int asked = a.n_new ? min(max(a.n_new[s], 0), a.n_tok) : a.n_tok;
-    const bool live = i < n;
-    if (!live && i < asked && u == 0 && hh0 == 0) raise_error(CRS_DEVERR_CAPACITY);
-    const int slot = len + i;
-    const int position = a.c.next_pos[s] + i;
-    const int row = live && hh0 < 2 * n_kv ? cache_row(a.c, s, slot) : -1;
-    float c[V], sn[V];
-    if (at.rot && live) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            rope_angle(position, a.inv_freq[u * V + j], a.mscale, a.inverse != 0, c[j], sn[j]);
-    }
-    for (int hh = hh0; hh < hh1; hh += kRopeBatch) {
-        P x[kRopeBatch], y[kRopeBatch];
-        __nv_bfloat16 *dst[kRopeBatch];
-#pragma unroll
-        for (int b = 0; b < kRopeBatch; ++b) {
-            const int h = hh + b;
-            dst[b] = nullptr;
-            if (h >= hh1) continue;
-            const __nv_bfloat16 *src;
-            if (h < 2 * n_kv) {
-                if (row < 0) continue;
-                const bool is_k = h < n_kv;
-                const int kh = is_k ? h : h - n_kv;
-                src = (is_k ? a.k + tok * a.ks : a.v + tok * a.vs) + (size_t)kh * D;
-                dst[b] = (is_k ? a.c.k : a.c.v) + ((size_t)row * n_kv + kh) * D;
-                if (is_k && u == 0) {
-                    const size_t m = ((size_t)s * n_kv + kh) * a.c.cap + slot;
-                    if (a.c.pos) a.c.pos[m] = position;
-                    if (a.c.mass) a.c.mass[m] = 0.0f;
-                }
-            } else {
-                src = a.q + tok * a.qs + (size_t)(h - 2 * n_kv) * D;
-                dst[b] = a.q_out + ((size_t)tok * a.n_q + (h - 2 * n_kv)) * D;
-            }
-            if (live) {
-                x[b].load(src + at.a);
-                if (at.rot) y[b].load(src + at.b);
-            } else {
-                x[b].w[0] = y[b].w[0] = make_uint4(0u, 0u, 0u, 0u);
+    extern __shared__ __align__(16) float rope_cs[];
+    __shared__ int rows[kApTokens];              // row in the pools; -1: no row; -2: not a token
+    const int half = a.rot_dim / 2, n_rot = half / V, n_kv = a.c.n_kv, D = a.c.D;
+    const RopeTable<V> table{rope_cs, a.tokens, n_rot};
+    const int all = a.c.n_seq * a.n_tok;
+    const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, all - t0);
+    const int h0 = blockIdx.y * a.per_group, nh = min(a.per_group, 2 * n_kv + a.n_q - h0);
+    if (threadIdx.x < nt) {
+        const int tok = t0 + threadIdx.x, s = tok / a.n_tok, i = tok - s * a.n_tok;
+        const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
+        const int asked = a.n_new ? min(max(a.n_new[s], 0), a.n_tok) : a.n_tok;
+        if (i >= n && i < asked && h0 == 0) raise_error(CRS_DEVERR_CAPACITY);
+        const bool stores = h0 < 2 * n_kv;
+        rows[threadIdx.x] = i >= n ? -2 : stores ? cache_row(a.c, s, len + i) : -1;
+        if (i < n) {
+            const int position = a.c.next_pos[s] + i;
+            for (int h = h0; h < min(n_kv, h0 + nh); ++h) {
+                const size_t m = ((size_t)s * n_kv + h) * a.c.cap + len + i;
+                if (a.c.pos) a.c.pos[m] = position;
+                if (a.c.mass) a.c.mass[m] = 0.0f;
             }
         }
+    }
+    for (int e = threadIdx.x; e < nt * half; e += kRopeThreads) {
+        const int t = e / half, j = e - t * half, tok = t0 + t, s = tok / a.n_tok;
+        float2 *to = table.pair(t, j);
+        rope_angle(a.c.next_pos[s] + (tok - s * a.n_tok), a.inv_freq[j], a.mscale, a.inverse != 0, to->x, to->y);
+    }
+    __syncthreads();
+    const int items = nt * a.per_group * (int)a.units.d;
+    for (int e0 = threadIdx.x; e0 < items; e0 += kRopeThreads * kRopeBatch) {
+        P x[kRopeBatch], y[kRopeBatch];
+        __nv_bfloat16 *dst[kRopeBatch];
+        int at_t[kRopeBatch], unit[kRopeBatch], off[kRopeBatch];     // unit -1: one vector, -2: two as they are; b - a
 #pragma unroll
-        for (int b = 0; b < kRopeBatch; ++b) {
-            if (!dst[b]) continue;
-            if (at.rot) {
-                const int h = hh + b;
-                if (live && (h < n_kv || h >= 2 * n_kv)) rope_turn<__nv_bfloat16, V, INTER>(x[b], y[b], c, sn);
-                y[b].store(dst[b] + at.b);
+        for (int q = 0; q < kRopeBatch; ++q) {
+            const int e = e0 + q * kRopeThreads;
+            dst[q] = nullptr;
+            if (e >= items) continue;
+            const int th = fd_quot(a.units, e), u = e - th * (int)a.units.d;
+            const int t = fd_quot(a.group, th), hg = th - t * (int)a.group.d, h = h0 + hg;
+            if (hg >= nh) continue;
+            const int row = rows[t];
+            const long long tok = t0 + t;
+            const RopeUnit<V, INTER> at(u, n_rot, a.rot_begin, a.rot_dim);
+            const __nv_bfloat16 *src;
+            bool turn = true;
+            if (h < 2 * n_kv) {
+                if (row < 0) continue;
+                turn = h < n_kv;
+                const int kh = turn ? h : h - n_kv;
+                src = (turn ? a.k + tok * a.ks : a.v + tok * a.vs) + (size_t)kh * D;
+                dst[q] = (turn ? a.c.k : a.c.v) + ((size_t)row * n_kv + kh) * D;
+            } else {
+                src = a.q + tok * a.qs + (size_t)(h - 2 * n_kv) * D;
+                dst[q] = a.q_out + ((size_t)tok * a.n_q + (h - 2 * n_kv)) * D;
             }
-            x[b].store(dst[b] + at.a);
+            if (row != -2) {
+                x[q].load(src + at.a);
+                if (at.rot) y[q].load(src + at.b);
+            } else {                             // the query row of a token that is not one: zeros
+                x[q].w[0] = y[q].w[0] = make_uint4(0u, 0u, 0u, 0u);
+                turn = false;
+            }
+            dst[q] += at.a;
+            off[q] = at.b - at.a;
+            at_t[q] = t;
+            unit[q] = !at.rot ? -1 : turn ? u : -2;
+        }
+#pragma unroll
+        for (int q = 0; q < kRopeBatch; ++q) {
+            if (!dst[q]) continue;
+            if (unit[q] >= 0) {
+                float2 cs[V];
+                table.load(at_t[q], unit[q], cs);
+                rope_turn<__nv_bfloat16, V, INTER>(x[q], y[q], cs);
+            }
+            if (unit[q] != -1) y[q].store(dst[q] + off[q]);
+            x[q].store(dst[q]);
         }
     }
 }
@@ -289,7 +376,6 @@ extern "C" int crs_rope(const crs_rope_params *p, int n_tok, int n_heads, int dt
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & (uintptr_t)(size - 1))
         return CRS_ERR_INVALID_ARG;
     const int v = (odd & 1) ? 1 : (odd & 2) ? 2 : (odd & 4) ? 4 : 8;
-    if (ceil_div_ll((long long)n_tok * p->D, kRopeThreads) > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define CRS_ROPE_CASE(T, V) \
     return rope_launch<T, V>(p, n_tok, n_heads, x, x_stride, pos, inv_freq, y, y_stride, s)
@@ -344,17 +430,22 @@ extern "C" int crs_cache_append(const crs_cache_params *p, const crs_cache_state
     a.rot_dim = r ? r->rot_dim : 0;
     a.inverse = r ? r->inverse : 0;
     a.mscale = r ? r->mscale : 1.0f;
-    a.units = a.rot_dim / 16 + (p->D - a.rot_dim) / 8;
-    const int heads = 2 * p->n_kv + a.n_q;
-    const long long items = (long long)p->n_seq * n_tok * a.units;
-    if (ceil_div_ll(items, kRopeThreads) > 0x7fffffffLL || heads > 65535) return CRS_ERR_UNSUPPORTED;
-    a.per_group = ceil_div(heads, rope_groups(items, heads, cache_sms()));
-    const dim3 grid((unsigned)ceil_div_ll(items, kRopeThreads), (unsigned)ceil_div(heads, a.per_group));
+    const int heads = 2 * p->n_kv + a.n_q, units = a.rot_dim / 16 + (p->D - a.rot_dim) / 8;
+    const long long toks = (long long)p->n_seq * n_tok;
+    if (toks > 0x7fffffffLL || heads > 65535) return CRS_ERR_UNSUPPORTED;
+    int groups;
+    rope_shape(toks, heads, units, a.rot_dim / 2, cache_sms(), a.tokens, groups);
+    a.tokens = min(a.tokens, kApTokens);
+    a.per_group = ceil_div(heads, groups);
+    a.units = fast_div(units);
+    a.group = fast_div(a.per_group);
+    const dim3 grid((unsigned)ceil_div_ll(toks, a.tokens), (unsigned)ceil_div(heads, a.per_group));
+    const size_t smem = (size_t)a.tokens * a.rot_dim * 4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     {
         ProfScope _ps(K_CACHE_APPEND, s);
-        if (r && r->interleaved) cache_append_kernel<true><<<grid, kRopeThreads, 0, s>>>(a);
-        else cache_append_kernel<false><<<grid, kRopeThreads, 0, s>>>(a);
+        if (r && r->interleaved) cache_append_kernel<true><<<grid, kRopeThreads, smem, s>>>(a);
+        else cache_append_kernel<false><<<grid, kRopeThreads, smem, s>>>(a);
     }
     CRS_CHECK_LAUNCH();
     return CRS_OK;

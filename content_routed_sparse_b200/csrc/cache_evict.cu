@@ -2,10 +2,10 @@
 // the others from the paged cache, sm_100a.
 //
 // Selection: one CTA per (sequence, KV head) holds the slots' order-preserving 32-bit
-// keys in registers, consecutive slots per warp.  The keep-th largest key is found from
-// the top, two bits per CTA-wide count, until few keys are left between, which one warp
-// finishes; a scan of the warps' counts above and at it, and ballots, place the kept
-// slots in ascending order, ties to the lower slot.  Longer caches than the registers hold re-read the keys from memory: four
+// keys in registers, consecutive slots per warp.  The keep-th largest key is bracketed by
+// a sample and found among the few keys in the bracket, by counts alone (no order of
+// arrival enters the result); a scan of the warps' counts above and at it, and
+// ballots, place the kept slots in ascending order, ties to the lower slot.  Longer caches than the registers hold re-read the keys from memory: four
 // passes with 256-bin histograms, then the same placement.
 //
 // Eviction: nothing depends on the order of a head's slots, so only the kept slots
@@ -52,26 +52,14 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *warp_sums, ui
     return inc - v + __shfl_sync(0xffffffffu, winc - w, warp);
 }
 
-constexpr int kMassList = 256;                   // keys that one warp searches
-
 // Warp w holds the 32 KPT slots from w 32 KPT, slot i 32 + lane of them in lane's key[i]:
 // loads and the kept slots' stores are contiguous, and ballots rank the slots in order.
-// CTA-wide sums of two values per thread, as cta_count
-__device__ __forceinline__ int2 cta_count2(int x, int y, int &ph) {
-    __shared__ int2 cbuf[2][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wx = __reduce_add_sync(0xffffffffu, x), wy = __reduce_add_sync(0xffffffffu, y);
-    if (lane == 0) cbuf[ph][warp] = make_int2(wx, wy);
-    __syncthreads();
-    const int2 v = lane < (int)(blockDim.x >> 5) ? cbuf[ph][lane] : make_int2(0, 0);
-    ph ^= 1;
-    return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
-}
-
 template <int THREADS, int KPT>
 __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
-    __shared__ uint32_t sums[32], list[kMassList], found;
-    __shared__ int listed;
+    // keys between at most, sample size, bins of the sample's histogram (in the list's place)
+    constexpr int kList = THREADS >= 1024 ? 6 * THREADS : 1024, kSample = THREADS >= 1024 ? 512 : 256;
+    constexpr int kBins = THREADS >= 1024 ? 4096 : 1024, kDigit = THREADS >= 1024 ? 20 : 22;
+    __shared__ uint32_t sums[32], pick[2], list[kList];
     const int sh = blockIdx.x, s = sh / a.n_kv, h = sh - s * a.n_kv;
     const int tid = threadIdx.x, lane = tid & 31;
     const int len = min(max(a.seq_len[s], 0), a.cap), k = min(a.keep, len);
@@ -109,60 +97,116 @@ __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
         }
     }
     if (nan) raise_error(CRS_DEVERR_NONFINITE);
-    // The largest threshold T that at least k keys reach, two bits at a time: n_lo keys reach
-    // T, n_hi reach T + 2^b.  Once few keys lie between, one warp finishes among them.
-    uint32_t T = 0u;
-    int n_lo = THREADS * KPT, n_hi = 0, b = 32, ph = 0;
-    while (b > 0 && n_lo - n_hi > kMassList) {
-        b -= 2;
-        int c12 = 0, c3 = 0;
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            c12 += key[i] >= T + (1u << b);
-            c12 += key[i] >= T + (2u << b) ? 0x10000 : 0;
-            c3 += key[i] >= T + (3u << b);
+    // T, the k-th largest key: c(lo) >= k > c(hi) is kept for c(x), the number of keys that
+    // reach x.  A sample (the first slot of some threads) gives a narrow pair lo, hi by a
+    // histogram of its top digits; the few keys between go to shared memory, and byte by byte
+    // histograms of them find T.  Where the sample misleads, or too many keys lie between,
+    // bisection over all keys goes on.
+    for (int e = tid; e < kBins; e += THREADS) list[e] = 0u;
+    __syncthreads();
+    if (tid % (THREADS / kSample) == 0) atomicAdd(&list[key[0] >> kDigit], 1u);
+    __syncthreads();
+    {
+        // the sample's ranks 3.5 deviations before and after k's (absent slots are sampled too)
+        const float share = (float)k / (float)(THREADS * KPT);
+        const float mid = share * kSample, dev = 3.5f * sqrtf(mid * (1.0f - share)) + 2.0f;
+        const uint32_t up = (uint32_t)max(0, (int)(mid - dev)), down = (uint32_t)(mid + dev) + 1u;
+        if (tid == 0) {
+            pick[0] = 0u;
+            pick[1] = 0xffffffffu;               // reached by protected slots only
         }
-        const int2 n = cta_count2(c12, c3, ph);
-        const int n1 = n.x & 0xffff, n2 = n.x >> 16, n3 = n.y;
-        if (n3 >= k) { T += 3u << b; n_lo = n3; }
-        else if (n2 >= k) { T += 2u << b; n_lo = n2; n_hi = n3; }
-        else if (n1 >= k) { T += 1u << b; n_lo = n1; n_hi = n2; }
-        else n_hi = n1;
-    }
-    if (b > 0) {
-        if (tid == 0) listed = 0;
-        __syncthreads();
+        constexpr int per = kBins / THREADS;
+        const int top = kBins - 1 - tid * per;   // this thread's bins, from the top
+        uint32_t sum = 0, total;
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            const bool in = (key[i] - T) >> b == 0u;
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            if (m == 0u) continue;
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&listed, __popc(m));
-            at = __shfl_sync(0xffffffffu, at, 0);
-            if (in) list[at + __popc(m & ((1u << lane) - 1u))] = key[i];   // the order does not matter
-        }
-        __syncthreads();
-        if (tid < 32) {
-            uint32_t mine[kMassList / 32];
-#pragma unroll
-            for (int i = 0; i < kMassList / 32; ++i) {
-                const int e = i * 32 + lane;
-                mine[i] = e < listed ? list[e] : 0u;
+        for (int e = 0; e < per; ++e) sum += list[top - e];
+        uint32_t above = cta_scan(sum, sums, total);
+        if ((above < up && up <= above + sum) || (above < down && down <= above + sum)) {
+            for (int e = 0; e < per; ++e) {
+                const uint32_t c = list[top - e];
+                const uint32_t from = (uint32_t)(top - e) << kDigit;
+                if (above < up && up <= above + c && top - e < kBins - 1) pick[1] = from + (1u << kDigit);
+                if (above < down && down <= above + c) pick[0] = from;
+                above += c;
             }
-            for (int q = b - 1; q >= 0; --q) {
-                const uint32_t cand = T | (1u << q);
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < kMassList / 32; ++i) n += mine[i] >= cand;
-                if (n_hi + __reduce_add_sync(0xffffffffu, n) >= k) T = cand;
-            }
-            if (lane == 0) found = T;
         }
         __syncthreads();
-        T = found;
     }
-    // slots past len have key 0 and follow every slot of the sequence: they lose every tie
+    uint32_t lo = pick[0], hi = pick[1];
+    int ph = 0;
+    auto reach = [&](uint32_t x) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) n += key[i] >= x;
+        return cta_count(n, ph);
+    };
+    int n_lo, n_hi;
+    {
+        uint32_t n = 0;                          // both counts at once: at most 2^15 keys
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) n += (key[i] >= lo ? 1u : 0u) + (key[i] >= hi ? 0x10000u : 0u);
+        n = (uint32_t)cta_count((int)n, ph);
+        n_lo = (int)(n & 0xffffu);
+        n_hi = (int)(n >> 16);
+    }
+    if (n_hi >= k) {                             // enough keys reach hi: T is hi or above
+        lo = hi;
+        n_lo = n_hi;
+        hi = 0xffffffffu;
+        n_hi = lo == hi ? 0 : reach(hi);
+        if (n_hi >= k) lo = hi;                  // protected slots alone
+    } else if (n_lo < k) {
+        hi = lo;
+        n_hi = n_lo;
+        lo = 0u;
+        n_lo = THREADS * KPT;
+    }
+    if (hi - lo > 1u && n_lo - n_hi <= kList) {
+        uint32_t mine = 0, total;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) mine += key[i] - lo < hi - lo;
+        uint32_t at = cta_scan(mine, sums, total);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i)
+            if (key[i] - lo < hi - lo) list[at++] = key[i] - lo;
+        __syncthreads();
+        constexpr int kFew = kList / THREADS;
+        const int n = n_lo - n_hi;
+        uint32_t few[kFew], left = (uint32_t)(k - n_hi), d = 0u;     // d: T - lo, its bytes so far
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) few[i] = i * THREADS + tid < n ? list[i * THREADS + tid] : 0u;
+        __syncthreads();
+        for (int shift = max(0, 24 - __clz(hi - lo - 1u)), up = 32;; up = shift, shift = max(0, shift - 8)) {
+            // the digit [shift, up) of the keys that share the bits from `up` on
+            if (tid < 256) list[tid] = 0u;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (i * THREADS + tid < n && (up == 32 || (few[i] ^ d) >> up == 0u))
+                    atomicAdd(&list[(few[i] >> shift) & ((1u << min(8, up - shift)) - 1u)], 1u);
+            __syncthreads();
+            const uint32_t own = tid < 256 ? list[255 - tid] : 0u;
+            const uint32_t above = cta_scan(own, sums, total);
+            if (above < left && left <= above + own) {
+                pick[0] = 255u - tid;
+                pick[1] = left - above;
+            }
+            __syncthreads();
+            d |= pick[0] << shift;
+            left = pick[1];
+            if (shift == 0) break;
+        }
+        lo += d;
+        hi = lo + 1u;
+    }
+    while (hi - lo > 1u) {
+        const uint32_t x = lo + ((hi - lo) >> 1);
+        if (reach(x) >= k) lo = x;
+        else hi = x;
+    }
+    const uint32_t T = lo;
+    // Slots past len have key 0 and follow every slot of the sequence: they lose every tie (a
+    // tie at key 0 that is kept whole, `ties` false, cannot include them: they count in it)
     uint32_t gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
@@ -174,15 +218,19 @@ __global__ void __launch_bounds__(THREADS) mass_select_kernel(MassSelArgs a) {
     uint32_t total;
     const uint32_t before = __shfl_sync(0xffffffffu, cta_scan(lane == 0 ? own : 0u, sums, total), 0);
     const uint32_t need = (uint32_t)k - (total & 0xffffu);
+    const bool ties = (total >> 16) != need;     // else every key equal to T is kept
     uint32_t eb = before >> 16, at = (before & 0xffffu) + min(eb, need);
     const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-        const uint32_t e = __ballot_sync(0xffffffffu, key[i] == T);
-        const bool take = key[i] > T || (key[i] == T && eb + __popc(e & lower) < need);
+        bool take = key[i] >= T;
+        if (ties) {
+            const uint32_t e = __ballot_sync(0xffffffffu, key[i] == T);
+            take = key[i] > T || (key[i] == T && eb + __popc(e & lower) < need);
+            eb += __popc(e);
+        }
         const uint32_t t = __ballot_sync(0xffffffffu, take);
         if (take) out[at + __popc(t & lower)] = j0 + i * 32;
-        eb += __popc(e);
         at += __popc(t);
     }
 }

@@ -1082,6 +1082,9 @@ def rope(x, pos, inv_freq, *, rot_begin: int = 0, interleaved: bool = False, msc
 
 
 # ----------------------------------------------------------- decode cache --
+_mass_params = functools.lru_cache(maxsize=256)(lambda *v: MassSelectParams(*v))
+
+
 def mass_select(mass, seq_len, keep: int, *, pos=None, next_pos=None, sink_end: int = 0, window: int = 0, idx=None,
                 count=None, stream=None):
     """The keep slots of each (sequence, KV head) with the most accumulated attention weight:
@@ -1102,12 +1105,18 @@ def mass_select(mass, seq_len, keep: int, *, pos=None, next_pos=None, sink_end: 
     elif sink_end > 0 or window > 0:
         raise ValueError("mass_select: sink_end and window need pos and next_pos")
     if idx is None:
-        idx = _empty((n_seq, n_kv, keep), torch.int32, mass.device, stream)
+        idx = seq_len.new_empty((n_seq, n_kv, keep)) if stream is None else \
+            _empty((n_seq, n_kv, keep), torch.int32, mass.device, stream)
+        idx_at = idx.data_ptr()
+    else:
+        idx_at = _want(idx, "idx", torch.int32, (n_seq, n_kv, keep), dev)
     if count is None:
-        count = _empty((n_seq,), torch.int32, mass.device, stream)
-    p = MassSelectParams(n_seq, n_kv, cap, int(keep), int(sink_end), int(window))
-    st = _c_mass_select(p, mass_at, pos_at, len_at, next_at, _want(idx, "idx", torch.int32, (n_seq, n_kv, keep), dev),
-                        _want(count, "count", torch.int32, (n_seq,), dev), _launch_stream(stream, dev))
+        count = torch.empty_like(seq_len) if stream is None else _empty((n_seq,), torch.int32, mass.device, stream)
+        count_at = count.data_ptr()
+    else:
+        count_at = _want(count, "count", torch.int32, (n_seq,), dev)
+    st = _c_mass_select(_mass_params(n_seq, n_kv, cap, int(keep), int(sink_end), int(window)), mass_at, pos_at, len_at,
+                        next_at, idx_at, count_at, _launch_stream(stream, dev))
     if st:
         raise CrsError("crs_mass_select", st)
     return idx, count
@@ -1209,7 +1218,10 @@ class KvCache:
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
                     _empty(qshape, torch.bfloat16, self.device, stream)
-            q_at, out_at = q.data_ptr(), _want(q_out, "q_out", torch.bfloat16, qshape, dev)
+                out_at = q_out.data_ptr()
+            else:
+                out_at = _want(q_out, "q_out", torch.bfloat16, qshape, dev)
+            q_at = q.data_ptr()
         elif q_out is not None:
             raise ValueError("append: q_out without q")
         if inv_freq is not None:
@@ -1254,13 +1266,17 @@ class KvCache:
         elif prefix_k is not prefix_v:
             raise ValueError("attend: prefix_k and prefix_v go together")
         if out is None:
-            out = torch.empty_like(q) if out_dtype is torch.bfloat16 and stream is None else \
+            out = torch.empty_like(q, dtype=out_dtype) if stream is None else \
                 _empty(shape, out_dtype, self.device, stream)
+            out_at = out.data_ptr()
+        else:
+            out_at = _want(out, "out", out.dtype, shape, dev)
         code = _dtype_code(out)
-        out_at = _want(out, "out", out.dtype, shape, dev)
         if lse is None:
             lse = _empty(shape[:3], torch.float32, self.device, stream)
-        lse_at = _want(lse, "lse", torch.float32, shape[:3], dev)
+            lse_at = lse.data_ptr()
+        else:
+            lse_at = _want(lse, "lse", torch.float32, shape[:3], dev)
         if mass_out is not None:
             if self.mass is None:
                 raise ValueError("attend: mass_out needs a cache that tracks mass")

@@ -2,6 +2,8 @@
 // addresses, and the host checks (sm_100a).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace crs {
@@ -71,14 +73,21 @@ inline int cache_check_state(const crs_cache_state *st) {
     return CRS_OK;
 }
 
-// SM count of the current device (148 where it cannot be read: the sizing stays valid).
+// SM count of the current device, looked up once per device (148 where it cannot be
+// read: the sizing stays valid).
 inline int cache_sms() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
-        sms = 148;
+        return 148;
     }
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 

@@ -42,7 +42,7 @@ template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(CaArgs a) {
     extern __shared__ __align__(128) unsigned char ca_smem[];
     static_assert(ca_per_sm<D>() * (ca_smem_bytes<D>() + (int)sizeof(CaLens) + 1024 + 64) <= 233472, "CTAs per SM");
-    constexpr int kTile = ca_tile_bytes<D>(), kChunks = D / 8;
+    constexpr int kTile = ca_tile_bytes<D>(), kChunks = D / 8, kParts = SPLIT ? 3 : 1;
     unsigned char *sK = ca_smem;                                       // [stages][64 rows][2 D bytes]
     unsigned char *sV = sK + kCaStages * kTile;
     float4 *sAcc = reinterpret_cast<float4 *>(sV + kCaStages * kTile); // [D / 8][32 lanes]
@@ -212,19 +212,20 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
                     o[j][2] *= c_hi; o[j][3] *= c_hi;
                 }
             }
-            // f32 output: P = P_hi + P_lo, both bf16 (about 16 significant bits); bf16 output:
-            // P rounded once, half a bf16 step, as the output itself is
-            uint32_t pa[4], pl[4];
-            if constexpr (SPLIT) {
-                pack_bf16_split(s[0][0], s[0][1], pa[0], pl[0]);
-                pack_bf16_split(s[0][2], s[0][3], pa[1], pl[1]);
-                pack_bf16_split(s[1][0], s[1][1], pa[2], pl[2]);
-                pack_bf16_split(s[1][2], s[1][3], pa[3], pl[3]);
-            } else {
-                pa[0] = pack_bf16(s[0][0], s[0][1]);
-                pa[1] = pack_bf16(s[0][2], s[0][3]);
-                pa[2] = pack_bf16(s[1][0], s[1][1]);
-                pa[3] = pack_bf16(s[1][2], s[1][3]);
+            // f32 output: P as three bf16 parts (24 bits); bf16 output: P rounded once, half a bf16
+            // step, as the output itself is
+            uint32_t pa[kParts][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x = s[q >> 1][(q & 1) * 2], y = s[q >> 1][(q & 1) * 2 + 1];
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                    pa[part][q] = *reinterpret_cast<const uint32_t *>(&h);
+                    const float2 back = __bfloat1622float2(h);
+                    x -= back.x;
+                    y -= back.y;
+                }
             }
 #pragma unroll
             for (int jj = 0; jj < D / 16; ++jj) {
@@ -232,11 +233,10 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
                 const int mi = lane >> 3, r = kw + (lane & 7) + ((mi & 1) << 3), c = jj * 2 + (mi >> 1);
                 uint32_t b0, b1, b2, b3;
                 ldsm_x4_t(vb + ca_off<D>(r, c), b0, b1, b2, b3);
-                mma_bf16(o[2 * jj], pa, b0, b1);
-                mma_bf16(o[2 * jj + 1], pa, b2, b3);
-                if constexpr (SPLIT) {
-                    mma_bf16(o[2 * jj], pl, b0, b1);
-                    mma_bf16(o[2 * jj + 1], pl, b2, b3);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    mma_bf16(o[2 * jj], pa[part], b0, b1);
+                    mma_bf16(o[2 * jj + 1], pa[part], b2, b3);
                 }
             }
         } else if (a.logits && !cur.prefix) {

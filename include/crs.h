@@ -700,9 +700,9 @@ int crs_cache_commit(const crs_cache_params *p, const crs_cache_state *st, int n
  *   mass_out[s, h, j] = decay * mass[s, h, j] + sum over its rows of the weight of j;
  * other slots are left as they were.
  * Arithmetic: products of bf16 values summed in fp32; softmax statistics in fp32;
- * the unnormalised weights enter the second product as bf16 when O is bf16 (an
- * error below that of the output's own rounding) and as a bf16 value plus a bf16
- * residual when O is f32.
+ * the unnormalised weights enter the second product as bf16 when O is bf16 (one
+ * rounding, the size of the output's own) and as three bf16 parts, 24 bits, when
+ * O is f32.
  * ====================================================================== */
 typedef struct {
     crs_cache_params c;

@@ -151,8 +151,12 @@ __device__ __forceinline__ int ca_units(int tiles) { return tiles > 0 ? tiles + 
 __device__ __forceinline__ long long ca_prefix_units(const CaArgs &a) {
     return (long long)a.c.n_kv * a.PRT * ca_units(a.PT);
 }
+// n / d of numbers >= 0, with the short division where both fit
+__device__ __forceinline__ long long ca_div(long long n, long long d) {
+    return ((n | d) >> 32) == 0 ? (long long)((uint32_t)n / (uint32_t)d) : n / d;
+}
 __device__ __forceinline__ long long ca_share(const CaArgs &a, long long W) {
-    return W > a.grid ? (W + a.grid - 1) / a.grid : 1;
+    return W > a.grid ? ca_div(W + a.grid - 1, a.grid) : 1;
 }
 
 // What a CTA keeps of the sequences' lengths, in shared memory: where its share starts, and
@@ -298,7 +302,7 @@ __device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const CaLens &L) {
     if (n0 >= W) return u;
     long long r;
     if (u.prefix) {
-        const int U = ca_units(a.PT), x = (int)(n0 / U);
+        const int U = ca_units(a.PT), x = (int)ca_div(n0, U);
         u.h = x / a.PRT;
         u.rt = x - u.h * a.PRT;
         u.T = a.PT;
@@ -308,7 +312,7 @@ __device__ __forceinline__ CaCursor ca_seek(const CaArgs &a, const CaLens &L) {
         u.T = ca_tiles_of(a, L, u.s);
         const int U = ca_units(u.T);
         r = n0 - P - (long long)L.before * K;
-        const int y = (int)(r / U);
+        const int y = (int)ca_div(r, U);
         r -= (long long)y * U;
         u.h = y / a.RT;
         u.rt = y - u.h * a.RT;

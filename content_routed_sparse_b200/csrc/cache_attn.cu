@@ -339,7 +339,7 @@ __device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, in
         const long long x = ((long long)s * a.c.n_kv + h) * a.RT + rt;
         const long long first = P + (long long)before * a.c.n_kv * a.RT +
                                 ((long long)h * a.RT + rt) * (T + kItemCost) + kItemCost;
-        const long long c0 = first / w, c1 = (first + T - 1) / w;
+        const long long c0 = ca_div(first, w), c1 = ca_div(first + T - 1, w);
         m.own0 = c0 + (long long)a.c.n_kv * a.PRT + x;
         m.n_own = (int)(c1 - c0 + 1);
     }
@@ -349,7 +349,7 @@ __device__ __forceinline__ MgRow mg_row(const CaArgs &a, int s, int h, int R, in
         const int prt = (int)(Rg / kCaRows);
         m.r_pre = (int)(Rg - (long long)prt * kCaRows);
         const long long x = (long long)h * a.PRT + prt, first = x * ca_units(a.PT) + kItemCost;
-        const long long c0 = first / w, c1 = (first + a.PT - 1) / w;
+        const long long c0 = ca_div(first, w), c1 = ca_div(first + a.PT - 1, w);
         m.pre0 = c0 + x;
         m.n_pre = (int)(c1 - c0 + 1);
     } else {

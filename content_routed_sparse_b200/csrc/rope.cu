@@ -48,23 +48,29 @@ __device__ __forceinline__ void rope_angle(int pos, double inv_freq, float mscal
     s *= inverse ? -mscale : mscale;
 }
 
-// Where unit u of a head's row lies: units [0, n_rot) are V pairs (vectors at a and
-// b), the rest V copied elements at a.
+// Where unit u of a head's row lies: units [0, n_rot) are V pairs (vectors at a and b), the
+// rest copied: two vectors each where they come in pairs on both sides of the rotated dims,
+// else one at a.
 template <int V, bool INTER> struct RopeUnit {
     int a, b;
-    bool rot;
-    __device__ __forceinline__ RopeUnit(int u, int n_rot, int rot_begin, int rot_dim) {
+    bool rot, two;
+    __device__ __forceinline__ RopeUnit(int u, int n_rot, int rot_begin, int rot_dim, int copied) {
         rot = u < n_rot;
+        two = rot || copied > V;
         if (rot) {
             a = rot_begin + u * (INTER ? 2 * V : V);
             b = a + (INTER ? V : rot_dim / 2);
         } else {
-            a = (u - n_rot) * V;
+            a = (u - n_rot) * copied;
             if (a >= rot_begin) a += rot_dim;
-            b = a;
+            b = a + V;
         }
     }
 };
+// elements of a copied unit
+inline int rope_copied(const int D, const int rot_begin, const int rot_dim, const int V) {
+    return rot_begin % (2 * V) == 0 && (D - rot_begin - rot_dim) % (2 * V) == 0 ? 2 * V : V;
+}
 
 // The angles of a CTA's tokens, in shared memory: (cos, sin) of two pairs to 16 bytes (of
 // one to 8 when V is 1), the pieces of a unit's V pairs apart, so that the threads of
@@ -148,7 +154,7 @@ template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 rope_kernel(const T *x, T *y, const int32_t *__restrict__ pos, const double *__restrict__ inv_freq, int n_tok, int heads,
             int tokens, int per_group, int D, int rot_begin, int rot_dim, long long xs, long long ys, float mscale,
-            int inverse, FastDiv units, FastDiv group) {
+            int inverse, int copied, FastDiv units, FastDiv group) {
     extern __shared__ __align__(16) float rope_cs[];
     const int half = rot_dim / 2, n_rot = half / V;
     const RopeTable<V> table{rope_cs, tokens, n_rot};
@@ -164,7 +170,7 @@ rope_kernel(const T *x, T *y, const int32_t *__restrict__ pos, const double *__r
     for (int e0 = threadIdx.x; e0 < items; e0 += kRopeThreads * kRopeBatch) {
         Pack<T, V> a[kRopeBatch], b[kRopeBatch];
         T *dst[kRopeBatch];
-        int tok[kRopeBatch], unit[kRopeBatch], off[kRopeBatch];      // (unit -1: copied), b's offset from a
+        int tok[kRopeBatch], unit[kRopeBatch], off[kRopeBatch];      // unit -1: one copied, -2: two; b - a
 #pragma unroll
         for (int q = 0; q < kRopeBatch; ++q) {
             const int e = e0 + q * kRopeThreads;
@@ -173,14 +179,14 @@ rope_kernel(const T *x, T *y, const int32_t *__restrict__ pos, const double *__r
             const int th = fd_quot(units, e), u = e - th * (int)units.d;
             const int t = fd_quot(group, th), h = th - t * (int)group.d;
             if (h >= nh) continue;
-            const RopeUnit<V, INTER> at(u, n_rot, rot_begin, rot_dim);
+            const RopeUnit<V, INTER> at(u, n_rot, rot_begin, rot_dim, copied);
             const T *row = x + (t0 + t) * xs + (long long)(h0 + h) * D;
             a[q].load(row + at.a);
-            if (at.rot) b[q].load(row + at.b);
+            if (at.two) b[q].load(row + at.b);
             dst[q] = y + (t0 + t) * ys + (long long)(h0 + h) * D + at.a;
             off[q] = at.b - at.a;
             tok[q] = t;
-            unit[q] = at.rot ? u : -1;
+            unit[q] = at.rot ? u : at.two ? -2 : -1;
         }
 #pragma unroll
         for (int q = 0; q < kRopeBatch; ++q) {
@@ -189,8 +195,8 @@ rope_kernel(const T *x, T *y, const int32_t *__restrict__ pos, const double *__r
                 float2 cs[V];
                 table.load(tok[q], unit[q], cs);
                 rope_turn<T, V, INTER>(a[q], b[q], cs);
-                b[q].store(dst[q] + off[q]);
             }
+            if (unit[q] != -1) b[q].store(dst[q] + off[q]);
             a[q].store(dst[q]);
         }
     }
@@ -218,7 +224,8 @@ inline void rope_shape(long long n_tok, int heads, int units, int half, int sms,
 template <typename T, int V>
 int rope_launch(const crs_rope_params *p, int n_tok, int heads, const void *x, long long xs, const int32_t *pos,
                 const double *inv_freq, void *y, long long ys, cudaStream_t s) {
-    const int half = p->rot_dim / 2, units = half / V + (p->D - p->rot_dim) / V;
+    const int half = p->rot_dim / 2, copied = rope_copied(p->D, p->rot_begin, p->rot_dim, V);
+    const int units = half / V + (p->D - p->rot_dim) / copied;
     int tokens, groups;
     rope_shape(n_tok, heads, units, half, cache_sms(), tokens, groups);
     const int per_group = ceil_div(heads, groups);
@@ -229,7 +236,7 @@ int rope_launch(const crs_rope_params *p, int n_tok, int heads, const void *x, l
     auto kern = p->interleaved ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
     kern<<<grid, kRopeThreads, smem, s>>>(static_cast<const T *>(x), static_cast<T *>(y), pos, inv_freq, n_tok, heads,
                                           tokens, per_group, p->D, p->rot_begin, p->rot_dim, xs, ys, p->mscale,
-                                          p->inverse, du, dg);
+                                          p->inverse, copied, du, dg);
     return cudaGetLastError() == cudaSuccess ? CRS_OK : CRS_ERR_CUDA;
 }
 
@@ -249,7 +256,7 @@ struct AppendArgs {
     long long ks, vs, qs;
     const double *inv_freq;
     const int32_t *n_new;
-    int n_tok, n_q, rot_begin, rot_dim, tokens, per_group, inverse;
+    int n_tok, n_q, rot_begin, rot_dim, tokens, per_group, inverse, copied;
     float mscale;
     FastDiv units, group;
 };
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) cache_append_kernel(
             if (hg >= nh) continue;
             const int row = rows[t];
             const long long tok = t0 + t;
-            const RopeUnit<V, INTER> at(u, n_rot, a.rot_begin, a.rot_dim);
+            const RopeUnit<V, INTER> at(u, n_rot, a.rot_begin, a.rot_dim, a.copied);
             const __nv_bfloat16 *src;
             bool turn = true;
             if (h < 2 * n_kv) {
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) cache_append_kernel(
             }
             if (row != -2) {
                 x[q].load(src + at.a);
-                if (at.rot) y[q].load(src + at.b);
+                if (at.two) y[q].load(src + at.b);
             } else {                             // the query row of a token that is not one: zeros
                 x[q].w[0] = y[q].w[0] = make_uint4(0u, 0u, 0u, 0u);
                 turn = false;
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) cache_append_kernel(
             dst[q] += at.a;
             off[q] = at.b - at.a;
             at_t[q] = t;
-            unit[q] = !at.rot ? -1 : turn ? u : -2;
+            unit[q] = !at.two ? -1 : at.rot && turn ? u : -2;
         }
 #pragma unroll
         for (int q = 0; q < kRopeBatch; ++q) {
@@ -430,7 +437,8 @@ extern "C" int crs_cache_append(const crs_cache_params *p, const crs_cache_state
     a.rot_dim = r ? r->rot_dim : 0;
     a.inverse = r ? r->inverse : 0;
     a.mscale = r ? r->mscale : 1.0f;
-    const int heads = 2 * p->n_kv + a.n_q, units = a.rot_dim / 16 + (p->D - a.rot_dim) / 8;
+    a.copied = rope_copied(p->D, a.rot_begin, a.rot_dim, 8);
+    const int heads = 2 * p->n_kv + a.n_q, units = a.rot_dim / 16 + (p->D - a.rot_dim) / a.copied;
     const long long toks = (long long)p->n_seq * n_tok;
     if (toks > 0x7fffffffLL || heads > 65535) return CRS_ERR_UNSUPPORTED;
     int groups;

@@ -231,3 +231,11 @@ def test_forced_wait_timeout_of_the_prefix_pass(crs, cuda_dev):
     assert flags & crs.DEVERR_TIMEOUT
     assert diag[0] > 0 and diag[1] == 1
     check(crs, cuda_dev, c, torch.float32)
+
+
+@pytest.mark.parametrize("n_seq,n_tok", [(129, 1), (300, 1), (260, 2)])
+def test_more_sequences_than_a_block_keeps(crs, cuda_dev, n_seq, n_tok):
+    """Past 128 sequences the lengths are scanned in pieces; many of them empty."""
+    lens = [(s * 37) % 91 if s % 3 else 0 for s in range(n_seq)]
+    c = make(cuda_dev, n_seq, n_tok, 2, 1, 64, 16, lens, 0, 15, ragged=n_tok > 1)
+    check(crs, cuda_dev, c, torch.float32)

@@ -23,7 +23,8 @@ constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaStages = 2;           // K/V tiles in the ring
 constexpr int kCaRing = kCaStages + 1; // tiles whose row lists are kept
 constexpr int kCaTcRows = 16;          // rows per KV head above which the prefix goes to the tensor cores
-constexpr int kMgThreads = 256;
+constexpr int kMgThreads = 128;
+constexpr int kMgSlots = 1024;         // slots whose mass a CTA updates at a time
 
 template <int D> constexpr int ca_tile_bytes() { return kCaKeys * D * 2; }
 template <int D> constexpr int ca_scratch_bytes() { return D / 8 * 32 * 16; }
@@ -368,11 +369,14 @@ __device__ __forceinline__ size_t mg_piece(const CaArgs &a, const MgRow &m, int 
     return ((size_t)(p - m.n_own) * a.c.n_kv + m.h) * ((size_t)a.c.n_seq * a.M) + (size_t)m.r_tc;
 }
 
-// Largest m and total l of the row's pieces (one warp; -inf and 0 when there is nothing).
+// Largest m and total l of the row's pieces, for LANES neighbouring lanes of a warp each
+// (all of its lanes take part; -inf and 0 when there is nothing).
+template <int LANES>
 __device__ __forceinline__ float2 mg_stat(const CaArgs &a, const MgRow &m, int lane) {
     const int n = m.n_own + m.n_pre;
     float mx = -INFINITY, l = 0.0f;
-    for (int p = lane; p < n; p += 32) {
+#pragma unroll 4
+    for (int p = lane % LANES; p < n; p += LANES) {
         bool tc;
         const size_t k = mg_piece(a, m, p, tc);
         const float2 v = *reinterpret_cast<const float2 *>((tc ? a.tc_ml : a.part_ml) + k * 2);
@@ -383,61 +387,52 @@ __device__ __forceinline__ float2 mg_stat(const CaArgs &a, const MgRow &m, int l
     }
     float Mx = mx;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) Mx = fmax_nan(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
-    l = warp_sum(mx == -INFINITY ? 0.0f : l * exp2f(mx - Mx));
+    for (int o = LANES / 2; o > 0; o >>= 1) Mx = fmax_nan(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
+    l = mx == -INFINITY ? 0.0f : l * exp2f(mx - Mx);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     return make_float2(Mx, l);
 }
 
-// CTA (sequence, KV head, chunk): joins the pieces of rows chunk, chunk + chunks, ... and
-// updates every chunks-th run of 512 slots' mass.  A row with few peers in its CTA has
-// several warps, each with a part of its pieces.
-template <int D, typename OutT>
-__global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int chunks) {
-    constexpr int kE = D / 32;
-    extern __shared__ float2 mg_stats[];         // [M] (m, l)
-    __shared__ float red[8][D];
+// The CTAs of one (sequence, KV head): `joins` join the pieces of its rows, WPR warps to a
+// row, the others update every chunks-th run of kMgSlots slots' mass.  The two kinds run
+// side by side: a row's statistics are found again where they are needed, which is less
+// than waiting for them.
+template <int D, int WPR, typename OutT>
+__global__ void __launch_bounds__(kMgThreads, 8) cache_merge_kernel(CaArgs a, int joins, int chunks) {
+    constexpr int kE = D / 32, kRows = kMgThreads / 32 / WPR;
+    extern __shared__ float mg_z[];              // mass: [M] lse in log2 units
+    __shared__ float red[WPR > 1 ? kMgThreads / 32 : 1][D];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int sh = blockIdx.x / chunks, chunk = blockIdx.x - sh * chunks;
+    const int sh = blockIdx.x / (joins + chunks), part = blockIdx.x - sh * (joins + chunks);
     const int s = sh / a.c.n_kv, h = sh - s * a.c.n_kv;
     wait_for_previous();
-    const int before = a.cum[s], after = a.cum[s + 1], all = a.cum[a.c.n_seq];
     const int len = cache_len(a.c, s), n = cache_new(a.c, a.n_new, a.n_tok, s, len);
     const int total = len + n, rows = n * a.G;
+    if (part >= joins && (part - joins) * kMgSlots >= total) return;
+    const int before = a.cum[s], after = a.cum[s + 1], all = a.cum[a.c.n_seq];
     const int T = after > before ? after - before - kItemCost : 0;
     const long long w = ca_share(a, ca_prefix_units(a) + (long long)all * a.c.n_kv * a.RT);
 
-    const bool mass = a.logits && chunk * 2 * kMgThreads < total;
-    const int step = mass ? 1 : chunks;          // the rows whose statistics are needed
-    for (int R = (mass ? 0 : chunk) + warp * step; R < rows; R += 8 * step) {
-        const MgRow m = mg_row(a, s, h, R, before, T, w);
-        const float2 st = mg_stat(a, m, lane);
-        if (lane == 0) mg_stats[R] = st;
-    }
-    __syncthreads();
-
-    const int mine = (a.M - chunk + chunks - 1) / chunks;      // rows of this CTA
-    const int wpr = mine >= 5 ? 1 : mine >= 3 ? 2 : mine == 2 ? 4 : 8;
-    const int sub = warp % wpr;
-    for (int q0 = 0; q0 < mine; q0 += 8 / wpr) {
-        const int q = q0 + warp / wpr, R = chunk + q * chunks;
-        const bool live = q < mine && R < rows;
+    if (part < joins) {
+        const int R = part * kRows + warp / WPR, sub = warp % WPR;
         float acc[kE];
 #pragma unroll
         for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
         float2 st = make_float2(-INFINITY, 0.0f);
-        if (live) {
-            st = mg_stats[R];
+        if (R < rows) {
             const MgRow m = mg_row(a, s, h, R, before, T, w);
+            st = mg_stat<32>(a, m, lane);
             const int np = m.n_own + m.n_pre;
             if (st.x != -INFINITY) {
                 // lane q knows the address and the weight of the warp's q-th piece
-                for (int p0 = sub; p0 < np; p0 += 32 * wpr) {
-                    const int mine_p = p0 + lane * wpr, count = min(32, (np - p0 + wpr - 1) / wpr);
+                for (int p0 = sub; p0 < np; p0 += 32 * WPR) {
+                    const int p = p0 + lane * WPR, count = min(32, (np - p0 + WPR - 1) / WPR);
                     const float *src = nullptr;
                     float f = 0.0f;
-                    if (mine_p < np) {
+                    if (p < np) {
                         bool tc;
-                        const size_t k = mg_piece(a, m, mine_p, tc);
+                        const size_t k = mg_piece(a, m, p, tc);
                         const float pm = (tc ? a.tc_ml : a.part_ml)[k * 2];
                         src = (tc ? a.tc_o : a.part_o) + k * D;
                         f = pm == -INFINITY ? 0.0f : exp2f(pm - st.x);
@@ -463,18 +458,18 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int c
                 }
             }
         }
-        if (wpr > 1) {
+        if constexpr (WPR > 1) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
             __syncthreads();
             if (sub == 0) {
-                for (int v = 1; v < wpr; ++v)
+#pragma unroll
+                for (int v = 1; v < WPR; ++v)
 #pragma unroll
                     for (int e = 0; e < kE; ++e) acc[e] += red[warp + v][lane * kE + e];
             }
-            __syncthreads();
         }
-        if (q < mine && sub == 0) {
+        if (R < a.M && sub == 0) {
             const int i = R / a.G, g = R - i * a.G;
             const size_t row = ((size_t)s * a.n_tok + i) * a.n_q + h * a.G + g;
             OutT *dst = static_cast<OutT *>(a.O) + row * D + lane * kE;
@@ -488,40 +483,47 @@ __global__ void __launch_bounds__(kMgThreads) cache_merge_kernel(CaArgs a, int c
             }
             if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (st.x + log2f(L)) * 0.6931471805599453f;
         }
+        return;
     }
-    if (!mass) return;
 
     // ---- mass: sum over the rows of 2^(logit - lse); a row that sees nothing adds 0
-    float *z = reinterpret_cast<float *>(mg_stats);
-    __syncthreads();
-    float zr[1024 / kMgThreads];
-#pragma unroll
-    for (int q = 0; q < 1024 / kMgThreads; ++q) {
-        const int R = tid + q * kMgThreads;
-        if (R < rows) {
-            const float2 st = mg_stats[R];
-            zr[q] = st.y != 0.0f ? st.x + log2f(st.y) : INFINITY;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 1024 / kMgThreads; ++q) {
-        const int R = tid + q * kMgThreads;
-        if (R < rows) z[R] = zr[q];
+    for (int R0 = 0; R0 < rows; R0 += kMgThreads / 8) {          // eight lanes to a row
+        const int R = R0 + tid / 8;
+        MgRow m = mg_row(a, s, h, min(R, rows - 1), before, T, w);
+        const float2 st = mg_stat<8>(a, m, lane);
+        if (tid % 8 == 0 && R < rows) mg_z[R] = st.y != 0.0f ? st.x + log2f(st.y) : INFINITY;
     }
     __syncthreads();
     const float *lg = a.logits + (size_t)sh * a.M * a.ls;
-    for (int j = (chunk * kMgThreads + tid) * 2; j < total; j += chunks * 2 * kMgThreads) {
-        float x = 0.0f, y = 0.0f;
-#pragma unroll 4
-        for (int R = 0; R < rows; ++R) {
-            const float2 v = *reinterpret_cast<const float2 *>(lg + (size_t)R * a.ls + j);
-            x += exp2f(v.x - z[R]);
-            y += exp2f(v.y - z[R]);
+    constexpr int kPairs = kMgSlots / (2 * kMgThreads);          // pairs of slots per thread
+    for (int j0 = (part - joins) * kMgSlots + tid * 2; j0 - tid * 2 < total; j0 += chunks * kMgSlots) {
+        float2 sum[kPairs], old[kPairs];
+        const size_t at = (size_t)sh * a.c.cap;
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+            const int j = j0 + q * 2 * kMgThreads;
+            sum[q] = make_float2(0.0f, 0.0f);
+            old[q].x = j < total ? a.c.mass[at + j] : 0.0f;
+            old[q].y = j + 1 < total ? a.c.mass[at + j + 1] : 0.0f;
         }
-        const size_t at = (size_t)sh * a.c.cap + j;
-        a.mass_out[at] = a.decay * a.c.mass[at] + x;
-        if (j + 1 < total) a.mass_out[at + 1] = a.decay * a.c.mass[at + 1] + y;
+#pragma unroll 2
+        for (int R = 0; R < rows; ++R) {
+            const float z = mg_z[R];
+#pragma unroll
+            for (int q = 0; q < kPairs; ++q) {
+                const int j = j0 + q * 2 * kMgThreads;
+                if (j >= total) continue;
+                const float2 v = *reinterpret_cast<const float2 *>(lg + (size_t)R * a.ls + j);
+                sum[q].x += exp2f(v.x - z);
+                sum[q].y += exp2f(v.y - z);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+            const int j = j0 + q * 2 * kMgThreads;
+            if (j < total) a.mass_out[at + j] = a.decay * old[q].x + sum[q].x;
+            if (j + 1 < total) a.mass_out[at + j + 1] = a.decay * old[q].y + sum[q].y;
+        }
     }
 }
 
@@ -591,17 +593,23 @@ template <int D, bool SPLIT> int ca_launch(const CaArgs &a, cudaStream_t s) {
     return CRS_OK;
 }
 
-template <int D, typename OutT> int mg_launch(const CaArgs &a, cudaStream_t s) {
+template <int D, int WPR, typename OutT> int mg_launch_rows(const CaArgs &a, cudaStream_t s) {
     const long long sh = (long long)a.c.n_seq * a.c.n_kv;
-    // one wave (four CTAs fit on an SM), as far as there are rows and slots to spread
-    const long long want = (long long)cache_sms() * 4 / sh;
-    const long long most = max(a.M, a.logits ? ceil_div(a.c.cap, 2 * kMgThreads) : 1);
-    const int chunks = (int)max(1LL, min(want, most));
-    if (sh * chunks > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
+    const int joins = ceil_div(a.M * WPR, kMgThreads / 32);
+    // the mass of up to two waves of CTAs (eight fit on an SM), more slots to a CTA beyond that
+    const long long most = max(1LL, (long long)cache_sms() * 16 / sh);
+    const int chunks = a.logits ? (int)min(most, (long long)ceil_div(a.c.cap, kMgSlots)) : 0;
+    const long long ctas = sh * (joins + chunks);
+    if (ctas > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
     ProfScope _ps(K_CACHE_MERGE, s);
-    CRS_TRY_CUDA(launch_chained(cache_merge_kernel<D, OutT>, (unsigned)(sh * chunks), kMgThreads, (size_t)a.M * 8, s, true,
-                                a, chunks));
+    CRS_TRY_CUDA(launch_chained(cache_merge_kernel<D, WPR, OutT>, (unsigned)ctas, kMgThreads, (size_t)a.M * 4, s, true, a,
+                                joins, chunks));
     return CRS_OK;
+}
+template <int D, typename OutT> int mg_launch(const CaArgs &a, cudaStream_t s) {
+    // one warp per row while the rows fill the GPU, else four share a row's pieces
+    const long long rows = (long long)a.c.n_seq * a.c.n_kv * a.M;
+    return rows >= (long long)cache_sms() * 8 ? mg_launch_rows<D, 1, OutT>(a, s) : mg_launch_rows<D, 4, OutT>(a, s);
 }
 
 }  // namespace crs

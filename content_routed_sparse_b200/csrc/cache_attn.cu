@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     int listed = 0;
 
     const size_t tok_stride = (size_t)a.c.n_kv * D;
+    // slots are read once per step: the partial results and the logits shall stay in L2 instead
+    const uint64_t once = evict_first_policy();
     // rows of the ahead tile into ring slot i % kCaRing
     auto list_tile = [&](int i) {
         if (!ahead.more()) return;
@@ -101,8 +103,8 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
                 const int row = sRow[slot * kCaKeys + r];
                 const bool ok = row >= 0;
                 const size_t off = ok ? (size_t)row * tok_stride + c * 8 : 0;
-                cp_async16_zfill(sK + buf * kTile + ca_off<D>(r, c), Kb + off, ok);
-                cp_async16_zfill(sV + buf * kTile + ca_off<D>(r, c), Vb + off, ok);
+                cp_async16_zfill_once(sK + buf * kTile + ca_off<D>(r, c), Kb + off, ok, once);
+                cp_async16_zfill_once(sV + buf * kTile + ca_off<D>(r, c), Vb + off, ok, once);
             }
         }
         cp_async_commit();

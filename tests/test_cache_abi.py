@@ -102,6 +102,8 @@ def test_attention_refusals(crs):
                      (dict(out_dtype=7), INVALID), (dict(n_q=3), UNSUPPORTED), (dict(n_q=130), UNSUPPORTED),
                      (dict(n_tok=600), UNSUPPORTED)):
         assert attn_call(crs, attn(crs, **kw)) == want
+    huge = cache(crs, n_seq=4096, page_size=1 << 20, max_pages=2000, n_pages=1, cap=2000 << 20)
+    assert attn_call(crs, attn(crs, huge)) == UNSUPPORTED                 # units past 32 bits
     p = attn(crs)
     for n in BAD_STATES:
         assert attn_call(crs, p, state(crs, **{n: None})) == INVALID

@@ -239,3 +239,36 @@ def test_more_sequences_than_a_block_keeps(crs, cuda_dev, n_seq, n_tok):
     lens = [(s * 37) % 91 if s % 3 else 0 for s in range(n_seq)]
     c = make(cuda_dev, n_seq, n_tok, 2, 1, 64, 16, lens, 0, 15, ragged=n_tok > 1)
     check(crs, cuda_dev, c, torch.float32)
+
+
+def test_two_streams_and_a_graph_at_once(crs, cuda_dev):
+    """The chained kernels of two calls on two streams, and of a captured graph beside them,
+    keep apart: every run has the bits of a lone one."""
+    cs = [make(cuda_dev, 24, 1, 8, 2, 128, 16, [(11 * s + k) % 150 for s in range(24)], 700 + k, 16 + k,
+               poison=False) for k in range(3)]
+    runs = [on(cuda_dev, c, crs) for c in cs]
+    alone = []
+    for d, cache in runs:
+        m = d["mass"].clone()
+        alone.append(cache.attend(d["q"], d["pk"], d["pv"], out_dtype=torch.bfloat16, mass_out=m) + (m,))
+    torch.cuda.synchronize()
+    d, cache = runs[2]
+    gm = d["mass"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go, gl = cache.attend(d["q"], d["pk"], d["pv"], out_dtype=torch.bfloat16, mass_out=gm)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        out = []
+        for (d, cache), s in zip(runs[:2], streams):
+            with torch.cuda.stream(s):
+                m = d["mass"].clone()
+                out.append(cache.attend(d["q"], d["pk"], d["pv"], out_dtype=torch.bfloat16, mass_out=m) + (m,))
+        with torch.cuda.stream(streams[2]):
+            gm.copy_(runs[2][0]["mass"])
+            graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(out + [(go, gl, gm)], alone):
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+    assert crs.get_device_error() == 0

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     CaCursor ahead = ca_seek(a, lens);           // next tile whose rows are listed
     CaCursor cur = ahead;                        // tile being consumed
     if (!cur.more()) {
-        wait_for_previous();
+        if (blockIdx.x == 0) wait_for_previous();
         return;
     }
     int listed = 0;
@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
         ca_advance(a, lens, cur);
     }
     cp_async_wait<0>();
-    wait_for_previous();                         // the merge waits for this kernel, and so for the prefix pass too
+    // The merge waits for this kernel, so one CTA of it waits for the prefix pass (all of them
+    // would keep their places on SMs that the prefix pass leaves free).
+    if (blockIdx.x == 0) wait_for_previous();
 }
 
 // --------------------------------------------------------------------------- merge --

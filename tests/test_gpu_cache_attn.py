@@ -9,7 +9,7 @@ Tolerances.  With exact weights p_j (sum 1) and output O = sum p_j v_j, A = sum 
  * sums of the weights and of p v: chains of at most 2^7 tensor-core steps per piece with at most
    one fp32 step (2^-23, truncated) each, and a few joins: 2^-15 A.
  * weights rounded to bf16 (half a step: 2^-8 relative before normalisation): 2^-8 A; split into
-   two bf16 values: the residual's half step, 2^-17 A at most.
+   three bf16 parts: the last residual's half step, below the 2^-17 A allowed here.
  * the output's own half step: 2^-8 |O| in bf16, 2^-24 |O| in f32.
 So |O' - O| <= A (2^-14 + 2^-17) for f32, A (2^-14 + 2^-8) + 2^-8 |O| for bf16; lse is off by
 2^-15 + |lse| 2^-22, an accumulated weight by 2^-14 of the sum of its contributions and 2^-23 of

@@ -244,10 +244,22 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
                 const int mi = lane >> 3, r = kw + (lane & 7) + ((mi & 1) << 3), c = jj * 2 + (mi >> 1);
                 uint32_t b0, b1, b2, b3;
                 ldsm_x4_t(vb + ca_off<D>(r, c), b0, b1, b2, b3);
+                if constexpr (SPLIT) {
+                    // the tensor core truncates what it adds to: short chains, joined with rounding
+                    float t[2][4] = {};
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    mma_bf16(o[2 * jj], pa[part], b0, b1);
-                    mma_bf16(o[2 * jj + 1], pa[part], b2, b3);
+                    for (int part = kParts - 1; part >= 0; --part) {
+                        mma_bf16(t[0], pa[part], b0, b1);
+                        mma_bf16(t[1], pa[part], b2, b3);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[2 * jj][e] += t[0][e];
+                        o[2 * jj + 1][e] += t[1][e];
+                    }
+                } else {
+                    mma_bf16(o[2 * jj], pa[0], b0, b1);
+                    mma_bf16(o[2 * jj + 1], pa[0], b2, b3);
                 }
             }
         } else if (a.logits && !cur.prefix) {
@@ -572,7 +584,8 @@ static CaPlan ca_plan(const crs_cache_attn_params *p) {
     const bool tc = p->prefix_len > 0 && rows > kCaTcRows;
     q.tc_tiles = (int)ceil_div_ll(rows, kPfRows);
     q.tc_splits = tc ? pf_splits(p->c.n_kv, q.tc_tiles, rows, D,
-                                 ceil_div(p->prefix_len, p->out_dtype == CRS_F32 ? 64 : 128), cache_sms())
+                                 ceil_div(p->prefix_len, p->out_dtype == CRS_F32 ? 64 : 128),
+                                 p->out_dtype == CRS_F32 ? ceil_div(p->prefix_len, kPfChain) : 1, cache_sms())
                      : 0;
     q.PT = tc ? 0 : ceil_div(p->prefix_len, kCaKeys);
     q.PRT = q.PT > 0 ? ceil_div(p->c.n_seq * q.M, kCaRows) : 0;

@@ -504,10 +504,16 @@ template <int D, bool SPLIT> int pf_launch(const CaArgs &a, cudaStream_t s) {
 // Key splits: the grid's waves times a split's length, against the partial results that
 // every split writes and the merge reads.  In microseconds, measured on one B200: a key
 // tile of 128 takes about 1.5, a CTA's start and end 5, the partial results 3 TB/s.
-inline int pf_splits(int n_kv, int tiles, long long rows, int D, int PT, int sms) {
-    int best = 1;
+//
+// The tensor core truncates each addition to an accumulator: an f32 output, whose three
+// parts of P add three times per 16 keys, is 3e-6 off after 1024 keys and 8.6e-6 after
+// 2900 (a plain fp32 product over 9000 to 26000 keys 1.7e-6 to 2.9e-6).  Its splits are at
+// most kPfChain keys long, and the merge adds them up with rounding.
+constexpr int kPfChain = 640;
+inline int pf_splits(int n_kv, int tiles, long long rows, int D, int PT, int least, int sms) {
+    int best = least;
     double best_cost = 1e30;
-    for (int sp = 1; sp <= PT && sp <= 2 * sms; ++sp) {
+    for (int sp = least; sp <= PT && sp <= max(least, 2 * sms); ++sp) {
         const long long ctas = (long long)n_kv * tiles * sp;
         const double waves = (double)((ctas + sms - 1) / sms);
         const double cost = waves * (((PT + sp - 1) / sp) * 1.5 + 5.0) + (double)sp * rows * n_kv * D * 8 / 3e6;

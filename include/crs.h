@@ -694,7 +694,9 @@ int crs_cache_commit(const crs_cache_params *p, const crs_cache_state *st, int n
  *   O = sum_j softmax_j(scale * q . k_j) v_j over both sets, lse the natural log
  * of the softmax's denominator.  The prefix K/V are read once for all rows: each
  * KV head's queries of the whole batch form one tall tile.  A row past n_new, and a
- * row that sees nothing, gets O = 0, lse = -inf.
+ * row that sees nothing, gets O = 0, lse = -inf.  Slots at and past a sequence's
+ * length with the new tokens may hold anything; the new tokens' own values must be
+ * finite, since a later one enters an earlier row's sums with weight 0.
  * mass_out (may be NULL; may be st->mass: in place): for every slot j of
  * sequence s below its length with the new tokens,
  *   mass_out[s, h, j] = decay * mass[s, h, j] + sum over its rows of the weight of j;

@@ -12,10 +12,12 @@
 // Warps: 0-7 and 8-15 are the streams' softmax (two threads per row, half of a tile's
 // keys each), 16 loads K/V tiles by TMA into a ring, 17 issues the products.  Per stream
 // and key tile: S = Q K^T to tensor memory; the softmax threads read their rows, keep a
-// running maximum that is raised only when a row outgrows it by 2^8 (the sums are exact
-// for any shift; O is rescaled in tensor memory then, a rare event), and write
-// P = 2^(S - m) over the S columns; O += P V takes P from tensor memory.  While one
-// stream's softmax runs, the other's products do.
+// running maximum m that is raised only when a row outgrows it by 2^8 (O is rescaled in
+// tensor memory then, a rare event), and write P = 2^(S - m) over the S columns; O += P V
+// takes P from tensor memory.  While one stream's softmax runs, the other's products do.
+// m starts as the exact fp32 maximum of the row's first tile, so that a weight of 1 or
+// more always exists however large the logits are: a bound rounded to bf16 exceeds logits
+// of 2^14 by more than the exponent's 126 and loses every weight of the row.
 //
 // Bound: up to 256 rows per KV head by memory (134 MB of K/V for 64 sequences with 4 heads
 // to a group: 41 us, of which 27 are the tiles at 5.5 TB/s), beyond that by the tensor
@@ -43,7 +45,8 @@ template <int D, bool SPLIT> struct PfCfg {
     static constexpr int kTile = kKeys * D * 2;              // bytes of a K or V tile
     static constexpr int kQ = 128 * D * 2;                   // bytes of a Q tile
     static constexpr int kStages = kTile >= 32768 ? 5 : 8;   // >= 5: see the order of use below
-    static constexpr int kSmem = 2 * kQ + kStages * kTile + 1024;
+    static constexpr int kTiles = 2 * kQ + kStages * kTile;
+    static constexpr int kSmem = kTiles + 3072;              // the tiles' alignment, PfTop, PfBars
     // tensor memory columns: S and the P over it, the parts of P that S cannot hold, O
     static constexpr int kPCols = kKeys / 2;
     static __host__ __device__ constexpr int s_col(int u) { return u * (SPLIT ? 128 : kKeys); }
@@ -56,10 +59,15 @@ static_assert(PfCfg<128, false>::kStages * PfCfg<128, false>::kTile >= 2 * 128 *
 
 struct PfBars {
     uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][2], o_full[2], drain;
-    __nv_bfloat16 top[2][2][128];                // [stream][half of a tile's keys][row]: maxima, rounded up
     uint32_t tmem;
     int abort;
 };
+typedef float PfTop[2][2][128];                  // [stream][half of a tile's keys][row]: maxima
+// All of it is dynamic shared memory: the tiles start `lead` bytes in, on a 1024-byte
+// boundary, PfTop follows them, PfBars take the lead where they fit there, else the end.
+// With a static part the tiles of D = 128 and bf16 output would not fit beside PfTop.
+static_assert(1008 + sizeof(PfTop) <= 3072 && sizeof(PfBars) + sizeof(PfTop) + sizeof(PfBars) <= 3072,
+              "PfTop always fits behind the tiles, PfBars before them or behind PfTop");
 
 // 2^x of two values on the FMA pipe, for a part of the weights, because the exponential
 // unit alone (16 a clock and SM) takes as long as the products: Cody and Waite's reduction
@@ -84,7 +92,8 @@ __device__ __forceinline__ float2 pf_exp2_poly(float2 x) {
     return p;
 }
 
-static_assert(PfCfg<128, false>::kSmem + sizeof(PfBars) <= 232448 && PfCfg<128, true>::kSmem + sizeof(PfBars) <= 232448,
+static_assert(PfCfg<128, false>::kSmem <= 232448 && PfCfg<128, true>::kSmem <= 232448 &&
+                  PfCfg<64, false>::kSmem <= 232448 && PfCfg<64, true>::kSmem <= 232448,
               "shared memory of one CTA");
 
 __device__ __forceinline__ float pf_max3(float a, float b, float c) {
@@ -108,10 +117,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     using C = PfCfg<D, SPLIT>;
     constexpr int KT = C::kKeys;
-    extern __shared__ unsigned char pf_raw[];
-    __shared__ PfBars B;
-    unsigned char *sQ = pf_raw + ((1024u - (smem_u32(pf_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(16) unsigned char pf_raw[];
+    const uint32_t lead = (1024u - (smem_u32(pf_raw) & 1023u)) & 1023u;
+    unsigned char *sQ = pf_raw + lead;
     unsigned char *ring = sQ + 2 * C::kQ;
+    PfTop &row_top = *reinterpret_cast<PfTop *>(sQ + C::kTiles);
+    PfBars &B = *reinterpret_cast<PfBars *>(lead >= sizeof(PfBars) ? pf_raw : sQ + C::kTiles + sizeof(PfTop));
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);      // uniform for the compiler too
     dependents_may_start();
@@ -320,15 +331,14 @@ cache_prefix_kernel(CaArgs a, const __grid_constant__ CUtensorMap tm_k, const __
                 for (int q = 0; q < 4; ++q) mx[q] = pf_max3(mx[q], v[e + q], v[e + 4 + q]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = fmax_nan(mx[q], v[HK - 4 + q]);
-            // both threads of the row take the same bound of its maximum, rounded up to bf16 (any
-            // shift will do); the other's is overwritten only after the products of both halves
-            const __nv_bfloat16 mine = __float2bfloat16_ru(fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3])));
-            B.top[u][hh][r] = mine;
+            // both threads of the row take the same maximum; the other's is overwritten only after
+            // the products of both halves
+            const float mine = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3]));
+            row_top[u][hh][r] = mine;
             tc::fence_before();
             meet();                              // S is read: P may overwrite it
             tc::fence_after();
-            const float top =
-                fmax_nan(__bfloat162float(mine), __bfloat162float(B.top[u][hh ^ 1][r])) * scale;
+            const float top = fmax_nan(mine, row_top[u][hh ^ 1][r]) * scale;
             if (i == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, !(top <= m + kPfSlack))) {

@@ -272,3 +272,55 @@ def test_two_streams_and_a_graph_at_once(crs, cuda_dev):
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
     assert crs.get_device_error() == 0
+
+
+def large_logits(c, n_seq, D, sign, own):
+    """Whole-numbered queries and keys, whose products are exact in fp32: dot products around
+    +-D 48^2, a few steps of 48 apart, so that several keys of a row count.  The own slots lie
+    `own` steps of about 48 above (below) the prefix."""
+    g = torch.Generator().manual_seed(21)
+    bump = lambda t: (torch.rand(t.shape, generator=g) < 1 / 64).float() * torch.where(  # noqa: E731
+        torch.rand(t.shape, generator=g) < 0.5, 1.0, -1.0)
+    c["q"] = torch.randint(40, 57, c["q"].shape, generator=g).to(torch.bfloat16)
+    c["pk"] = (sign * 48 + bump(c["pk"])).to(torch.bfloat16)
+    k = sign * 48 + bump(c["k"])
+    k[..., :abs(own)] += 1.0 if own > 0 else -1.0
+    c["k"] = k.to(torch.bfloat16)
+    return c
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [0.125, 1.0])
+@pytest.mark.parametrize("n_seq", [20, 70])
+def test_tensor_core_prefix_large_logits(crs, cuda_dev, out_dtype, D, scale, n_seq):
+    """Logits of 1.8e4 to 3e5 (natural), of both signs and rising from one to the other, with the
+    own slots above, at and below the prefix: 80 and 280 query rows per KV head.
+
+    The products are whole numbers below 2^24, exact in fp32.  The scaled logit of a slot is
+    rounded once, half a step of |z|: 2^-24 |z| relative in its weight, as much again in the
+    row's log-sum-exp (fp32), which enters the accumulated weights; the prefix's exponents are
+    formed by one FMA.  The scale's own rounding (2^-24) times the difference of two logits
+    that both count (under 2^5) is below 2^-18."""
+    for sign, own in ((1, 0), (1, 3), (1, -3), (-1, 2)):
+        c = make(cuda_dev, n_seq, 1, 8, 2, D, 16, [(5 * s) % 40 for s in range(n_seq)], 700, 20, poison=False)
+        c = large_logits(c, n_seq, D, sign, own)
+        if sign < 0:                             # from -3e5 to 3e5 within a row
+            c["pk"][350:] = -c["pk"][350:]
+        d, cache = on(cuda_dev, c, crs)
+        mo = d["mass"].clone()
+        O, lse = cache.attend(d["q"], d["pk"], d["pv"], scale=scale, out_dtype=out_dtype, mass_out=mo)
+        torch.cuda.synchronize()
+        assert crs.get_device_error() == 0
+        eO, el, em, A = ref.attend(c["q"], c["k"], c["v"], c["table"], c["seq_len"], c["cap"], None, c["pk"], c["pv"],
+                                   scale=scale, mass=c["mass"])
+        z = 2.0 * float(el.abs().max()) * 2.0 ** -24
+        half = 0.0 if out_dtype == torch.float32 else 2.0 ** -8
+        o = O.double().cpu()
+        tol = A * (2.0 ** -14 + 2.0 ** -17 + z + half) + eO.abs() * (half or 2.0 ** -24)
+        assert torch.isfinite(o).all() and ((o - eO).abs() <= tol).all(), (sign, own)
+        assert ((lse.double().cpu() - el).abs() <= el.abs() * 2.0 ** -22 + 2.0 ** -15).all()
+        got, add = mo.double().cpu(), (em - c["mass"].double()).abs()
+        for s in range(n_seq):
+            t = int(c["seq_len"][s]) + 1
+            assert ((got - em).abs() <= add * (2.0 ** -14 + z) + em.abs() * 2.0 ** -21)[s, :, :t].all()

@@ -324,3 +324,17 @@ def test_tensor_core_prefix_large_logits(crs, cuda_dev, out_dtype, D, scale, n_s
         for s in range(n_seq):
             t = int(c["seq_len"][s]) + 1
             assert ((got - em).abs() <= add * (2.0 ** -14 + z) + em.abs() * 2.0 ** -21)[s, :, :t].all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,n_seq", [(64, 20), (128, 20), (128, 70)])
+@pytest.mark.parametrize("column", range(0, 16, 3))
+def test_far_keys_of_the_prefix_add_nothing(crs, cuda_dev, out_dtype, D, n_seq, column):
+    """Keys some 500 to 1000 log2 units below the others, whose values are 2^126: their weight is
+    0 in any 32-bit form, so nothing of them may reach the output."""
+    c = make(cuda_dev, n_seq, 1, 8, 2, D, 16, [s % 9 for s in range(n_seq)], 400, 22, poison=False)
+    c["q"] = torch.full_like(c["q"], 4.0)
+    c["k"], c["pk"] = c["k"] * 0.125, c["pk"] * 0.125
+    c["pk"][column::16] = -12.0
+    c["pv"][column::16] = 2.0 ** 126
+    check(crs, cuda_dev, c, out_dtype, scale=0.125, with_mass=False)

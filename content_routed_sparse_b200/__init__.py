@@ -964,8 +964,8 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, factor: float = 1.0, scal
         def pair_of(turns):        # the pair that makes this many turns over the trained length
             return rot_dim * math.log(trained_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
+        # not cut to the pairs that exist: the slowest may still make many turns, the fastest few
         lo, hi = math.floor(pair_of(beta_fast)), math.ceil(pair_of(beta_slow))
-        lo, hi = max(lo, 0), min(hi, rot_dim // 2 - 1)
         ramp = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         f = f * (1.0 - ramp) + f / factor * ramp
     return f.to(device)

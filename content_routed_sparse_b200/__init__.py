@@ -1135,7 +1135,12 @@ class KvCache:
     The tensors are the caller's: k_pool, v_pool [n_pages, page_size, n_kv, D] bf16,
     block_table [n_seq, max_pages], seq_len, next_pos [n_seq] int32, pos [n_seq, n_kv, cap]
     int32 and mass [n_seq, n_kv, cap] f32 (both optional; without them cap is
-    max_pages * page_size).  KvCache.empty allocates them."""
+    max_pages * page_size).  KvCache.empty allocates them.  Assigning another tensor of the same
+    dtype, shape and device (cache.mass = ..., None for pos or mass: no longer tracked) takes
+    effect in every later call; a captured graph keeps the ones it was captured with."""
+
+    _TENSORS = {"k_pool": torch.bfloat16, "v_pool": torch.bfloat16, "block_table": torch.int32, "pos": torch.int32,
+                "mass": torch.float32, "seq_len": torch.int32, "next_pos": torch.int32}
 
     def __init__(self, k_pool, v_pool, block_table, seq_len, next_pos, pos=None, mass=None):
         _need(k_pool, "k_pool", torch.bfloat16)
@@ -1162,14 +1167,30 @@ class KvCache:
         for t in (v_pool, block_table, seq_len, next_pos, pos, mass):
             if t is not None and t.device != k_pool.device:
                 raise ValueError("the cache's tensors must be on one device")
-        self.k_pool, self.v_pool, self.block_table = k_pool, v_pool, block_table
-        self.seq_len, self.next_pos, self.pos, self.mass = seq_len, next_pos, pos, mass
         self.n_seq, self.n_kv, self.D, self.cap, self.device = n_seq, n_kv, D, cap, k_pool.device
         self.p = CacheParams(n_seq, n_kv, D, page_size, max_pages, n_pages, cap)
-        self.st = CacheState(*(t.data_ptr() if t is not None else None
-                               for t in (k_pool, v_pool, block_table, pos, mass, seq_len, next_pos)))
         self._dev = k_pool.get_device()
         self._attn = {}              # parameters and workspace size by problem
+        self.__dict__.update(k_pool=k_pool, v_pool=v_pool, block_table=block_table, pos=pos, mass=mass,
+                             seq_len=seq_len, next_pos=next_pos)
+        self._address()
+
+    def _address(self):
+        """The addresses that the calls are given."""
+        self.st = CacheState(*(None if t is None else t.data_ptr() for t in map(self.__dict__.get, self._TENSORS)))
+
+    def __setattr__(self, name, value):
+        dtype = self._TENSORS.get(name)
+        if dtype is None:
+            object.__setattr__(self, name, value)
+            return
+        if value is not None or name not in ("pos", "mass"):
+            old = self.__dict__[name]
+            _need(value, name, dtype, (self.n_seq, self.n_kv, self.cap) if old is None else old.shape)
+            if value.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}, got {value.device}")
+        self.__dict__[name] = value
+        self._address()
 
     @classmethod
     def empty(cls, n_seq, n_kv, max_len, D=128, page_size=64, first_pos=0, track=True, device="cuda"):

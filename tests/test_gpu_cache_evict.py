@@ -212,3 +212,35 @@ def test_a_generation_with_eviction(crs, cuda_dev):
             assert torch.equal(cache.pos.cpu(), ep) and torch.equal(cache.mass.cpu(), em)
     assert crs.get_device_error() == 0
     assert int(cache.next_pos[0]) == plen + 10 + 29 and int(cache.seq_len[0]) < 40
+
+
+def test_replaced_tensors_are_used(crs, cuda_dev):
+    """Every call after `cache.x = new` reads and writes the new tensor, and only it."""
+    g = torch.Generator().manual_seed(31)
+    n_seq, n_kv, D, cap = 3, 2, 64, 32
+    r = lambda *sh: torch.randn(sh, generator=g).to(torch.bfloat16).to(cuda_dev)  # noqa: E731
+    old = crs.KvCache.empty(n_seq, n_kv, cap, D=D, page_size=8, device=cuda_dev)
+    new = crs.KvCache.empty(n_seq, n_kv, cap, D=D, page_size=8, first_pos=5, device=cuda_dev)
+    new.block_table.copy_(new.block_table.flip(0))
+    names = ("k_pool", "v_pool", "block_table", "pos", "mass", "seq_len", "next_pos")
+    kept = {n: getattr(old, n).clone() for n in names}
+    first = {n: getattr(old, n) for n in names}
+    want = crs.KvCache(*(getattr(new, n).clone() for n in ("k_pool", "v_pool", "block_table", "seq_len", "next_pos")),
+                       pos=new.pos.clone(), mass=new.mass.clone())
+    for n in names:
+        setattr(old, n, getattr(new, n))
+    f = crs.rope_inv_freq(D)
+    for _ in range(12):
+        q, k, v = r(n_seq, 2, 4, D), r(n_seq, 2, n_kv, D), r(n_seq, 2, n_kv, D)
+        outs = []
+        for c in (old, want):
+            qr = c.append(k, v, q=q, inv_freq=f)
+            outs.append((qr,) + c.attend(qr, mass_out=c.mass))
+            c.commit(2)
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+    for c in (old, want):
+        c.evict(*c.select(10, window=2))
+    for n in names:
+        assert torch.equal(getattr(old, n), getattr(want, n))
+        assert torch.equal(first[n], kept[n])                  # the replaced ones are left alone
+    assert crs.get_device_error() == 0

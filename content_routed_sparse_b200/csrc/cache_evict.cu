@@ -315,13 +315,15 @@ constexpr int kEvBatch = 8;                      // row copies a warp keeps in f
 
 template <int D>
 __global__ void __launch_bounds__(kEvWarps * 32)
-cache_evict_kernel(CacheDev c, int keep, const int32_t *__restrict__ idx, const int32_t *__restrict__ count) {
+cache_evict_kernel(CacheDev c, int keep, const int32_t *__restrict__ idx, const int32_t *__restrict__ count,
+                   int blocks) {                 // CTAs per (sequence, KV head)
     constexpr int kLanes = D / 4;                // lanes per move: D / 8 for K, D / 8 for V
     constexpr int kPer = 32 / kLanes;            // moves per warp access
-    const int sh = blockIdx.y, s = sh / c.n_kv, h = sh - s * c.n_kv;
+    const int sh = blockIdx.x / blocks, block = blockIdx.x - sh * blocks;
+    const int s = sh / c.n_kv, h = sh - s * c.n_kv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = min(max(count[s], 0), min(keep, c.cap));
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) c.seq_len[s] = n;
+    if (block == 0 && h == 0 && threadIdx.x == 0) c.seq_len[s] = n;
     const int32_t *list = idx + (size_t)sh * keep;
     int lo = 0, hi = n;                          // entries below n
     while (lo < hi) {
@@ -330,7 +332,7 @@ cache_evict_kernel(CacheDev c, int keep, const int32_t *__restrict__ idx, const 
         else hi = mid;
     }
     const int stay = lo, moves = n - stay;
-    const int r = (blockIdx.x * kEvWarps + warp) * 32 + lane;
+    const int r = (block * kEvWarps + warp) * 32 + lane;
     if (r - lane >= moves) return;               // whole warps
     int src = -1, dst = -1;
     if (r < moves) {
@@ -412,16 +414,17 @@ extern "C" int crs_cache_evict(const crs_cache_params *p, const crs_cache_state 
     if ((e = cache_check_state(st))) return e;
     if (!idx || !count) return CRS_ERR_INVALID_ARG;
     const long long sh = (long long)p->n_seq * p->n_kv;
-    if (sh > 65535) return CRS_ERR_UNSUPPORTED;
     // n kept slots of cap: at most min(n, cap - n) move
     const int most = max(1, min(keep, p->cap / 2));
-    const dim3 grid((unsigned)ceil_div(most, kEvWarps * 32), (unsigned)sh);
+    const int blocks = ceil_div(most, kEvWarps * 32);
+    if (sh * blocks > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)(sh * blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const CacheDev c = cache_dev(p, st);
     {
         ProfScope _ps(K_CACHE_EVICT, s);
-        if (p->D == 128) cache_evict_kernel<128><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count);
-        else cache_evict_kernel<64><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count);
+        if (p->D == 128) cache_evict_kernel<128><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count, blocks);
+        else cache_evict_kernel<64><<<grid, kEvWarps * 32, 0, s>>>(c, keep, idx, count, blocks);
     }
     CRS_CHECK_LAUNCH();
     return CRS_OK;

@@ -244,3 +244,31 @@ def test_replaced_tensors_are_used(crs, cuda_dev):
         assert torch.equal(getattr(old, n), getattr(want, n))
         assert torch.equal(first[n], kept[n])                  # the replaced ones are left alone
     assert crs.get_device_error() == 0
+
+
+def test_many_heads(crs, cuda_dev):
+    """4096 sequences of 17 heads, four slots each, two kept: more (sequence, head) pairs than a
+    grid's second dimension holds."""
+    g = torch.Generator(device=cuda_dev).manual_seed(41)
+    n_seq, n_kv, D = 4096, 17, 64
+    cache = crs.KvCache.empty(n_seq, n_kv, 4, D=D, page_size=4, device=cuda_dev)
+    for t in (cache.k_pool, cache.v_pool):
+        t.copy_(torch.randint(-99, 99, t.shape, generator=g, device=cuda_dev))
+    cache.mass.copy_(torch.rand(cache.mass.shape, generator=g, device=cuda_dev))
+    cache.pos.copy_(torch.randint(0, 99, cache.pos.shape, generator=g, device=cuda_dev))
+    cache.seq_len.fill_(4)
+    idx, count = crs.mass_select(cache.mass, cache.seq_len, 2)       # by weight alone
+    best = cache.mass.sort(dim=-1, descending=True, stable=True).indices[..., :2].sort(dim=-1).values
+    assert torch.equal(idx.long(), best) and (count == 2).all()
+    # what slots 0 and 1 hold afterwards: themselves, or the r-th kept slot past them
+    a, b = best.unbind(-1)
+    first = torch.where(a == 0, a, torch.where(a == 1, b, a))
+    second = torch.where(a == 1, a, b)
+    src = torch.stack([first, second, torch.full_like(a, 2), torch.full_like(a, 3)], -1)
+    at = src.transpose(1, 2)[..., None].expand(-1, -1, -1, D)
+    want = [t.view(n_seq, 4, n_kv, D).gather(1, at) for t in (cache.k_pool, cache.v_pool)]
+    want += [t.gather(2, src) for t in (cache.pos, cache.mass)]
+    cache.evict(idx, count)
+    got = [t.view(n_seq, 4, n_kv, D) for t in (cache.k_pool, cache.v_pool)] + [cache.pos, cache.mass]
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and (cache.seq_len == 2).all()
+    assert crs.get_device_error() == 0

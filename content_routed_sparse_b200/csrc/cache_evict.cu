@@ -389,6 +389,11 @@ extern "C" int crs_mass_select(const crs_mass_select_params *p, const float *mas
     const long long ctas = (long long)p->n_seq * p->n_kv;
     if (ctas > 0x7fffffffLL) return CRS_ERR_UNSUPPORTED;
     if (!mass || !seq_len || !idx || !count || (pos && !next_pos)) return CRS_ERR_INVALID_ARG;
+    // a sequence's heads run side by side: what one writes, the others must not read
+    const void *in[4] = {mass, pos, seq_len, pos ? next_pos : nullptr};
+    for (const void *q : in)
+        if (q && (q == idx || q == count)) return CRS_ERR_INVALID_ARG;
+    if (idx == count) return CRS_ERR_INVALID_ARG;
     MassSelArgs a{mass, pos, seq_len, next_pos, idx, count, p->n_kv, p->cap, p->keep, p->sink_end, p->window};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)ctas;

@@ -746,7 +746,7 @@ typedef struct {
 
 /* mass [n_seq, n_kv, cap] f32; pos [n_seq, n_kv, cap] int32 or NULL; seq_len,
  * next_pos [n_seq] int32 (next_pos may be NULL when pos is); idx [n_seq, n_kv, keep]
- * int32; count [n_seq] int32. */
+ * int32; count [n_seq] int32; neither output may be one of the inputs. */
 int crs_mass_select(const crs_mass_select_params *p, const float *mass, const int32_t *pos, const int32_t *seq_len,
                     const int32_t *next_pos, int32_t *idx, int32_t *count, void *stream);
 

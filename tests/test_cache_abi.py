@@ -174,3 +174,14 @@ def test_row_strides(crs):
         rows(t.transpose(1, 2))
     with pytest.raises(ValueError):
         rows(t[:, :1].expand(3, 5, 8, 64))                                # stride 0
+
+
+def test_select_refuses_lengths_as_output(crs):
+    """The heads of a sequence run side by side: a count written over the lengths (or the next
+    positions) would be read by the others."""
+    L, S = crs.lib(), crs.MassSelectParams
+    at = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(6)]           # mass, pos, seq_len, next_pos, idx, count
+    for shared in ((5, 2), (5, 3), (4, 1), (4, 0), (4, 2), (4, 3), (5, 4)):
+        args = list(at)
+        args[shared[0]] = args[shared[1]]
+        assert L.crs_mass_select(by(S(2, 2, 8, 4, 0, 1)), *args, None) == INVALID, shared

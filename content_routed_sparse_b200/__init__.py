@@ -1055,7 +1055,8 @@ def rope(x, pos, inv_freq, *, rot_begin: int = 0, interleaved: bool = False, msc
          inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [n_tok, n_heads, D] bf16 or f32 (token rows may be strided), pos
     [n_tok] int32, inv_freq [rot_dim / 2] float64 -> the rotated x (new, or out; out=x
-    rotates in place).  inverse=True applies the transpose: the gradient of the call."""
+    rotates in place).  inverse=True applies the transpose: the gradient of the call, to be
+    called with the output's gradient (like every call here it records nothing for autograd)."""
     dev = _current(x, "x")
     shape = x.shape
     if len(shape) != 3:
@@ -1087,8 +1088,8 @@ _mass_params = functools.lru_cache(maxsize=256)(lambda *v: MassSelectParams(*v))
 
 def mass_select(mass, seq_len, keep: int, *, pos=None, next_pos=None, sink_end: int = 0, window: int = 0, idx=None,
                 count=None, stream=None):
-    """The keep slots of each (sequence, KV head) with the most accumulated attention weight:
-    mass [n_seq, n_kv, cap] f32 -> (idx [n_seq, n_kv, keep] int32 ascending, -1 pad; count
+    """The keep slots (1..cap; all of a shorter sequence) of each (sequence, KV head) with the most
+    accumulated attention weight: mass [n_seq, n_kv, cap] f32 -> (idx [n_seq, n_kv, keep] int32 ascending, -1 pad; count
     [n_seq] int32).  With pos [n_seq, n_kv, cap] and next_pos [n_seq] (int32), slots of
     positions below sink_end and of the last `window` positions are kept first."""
     dev = _current(mass, "mass")
@@ -1272,7 +1273,9 @@ class KvCache:
         """Attention of q [n_seq, n_tok, n_q, D] over the shared prefix [prefix_len, n_kv, D] and
         each sequence's slots, the appended tokens included (causally) -> (O in out_dtype,
         f32 or bf16, lse).  mass_out [n_seq, n_kv, cap] f32 (self.mass: in place) receives
-        decay * self.mass plus the weights the slots got."""
+        decay * self.mass plus the weights the slots got, from every token given.  Where drafts may
+        be rejected and only accepted tokens shall count: attend without mass_out, then again with
+        n_new=accepted and mass_out=self.mass, before commit(accepted, n_tok)."""
         dev = self._here()
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError(f"q must be [{self.n_seq}, n_tok, n_q, {self.D}]")

@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kCaThreads, ca_per_sm<D>()) cache_attn_kernel(
     int listed = 0;
 
     const size_t tok_stride = (size_t)a.c.n_kv * D;
-    // slots are read once per step: the partial results and the logits shall stay in L2 instead
+    // slots are read once per tile of 16 query rows (one tile in a step of few tokens): the
+    // partial results and the logits shall stay in L2 instead
     const uint64_t once = evict_first_policy();
     // rows of the ahead tile into ring slot i % kCaRing
     auto list_tile = [&](int i) {

@@ -72,11 +72,11 @@ static_assert(1008 + sizeof(PfTop) <= 3072 && sizeof(PfBars) + sizeof(PfTop) + s
 // 2^x of two values on the FMA pipe, for a part of the weights, because the exponential
 // unit alone (16 a clock and SM) takes as long as the products: Cody and Waite's reduction
 // x = n + f, |f| <= 1/2 (n by adding and subtracting 1.5 2^23), a minimax polynomial of
-// degree 4 for 2^f (largest relative error 2.6e-6, fitted by reweighted least squares on
-// Chebyshev nodes), and n added to the exponent.  x below kPfPolyLeast becomes it: there
-// n = -127, the polynomial of f = 2^-17 is 33 steps above 1, and its exponent field ends at
-// 0, so the value is 33 2^-149, which is 0 in bf16: a key too far to count adds nothing,
-// however large its V.  Between it and 2^-126 the value is off by up to 2^-127.
+// degree 4 for 2^f (largest relative error 2.7e-6 as evaluated, fitted by reweighted least
+// squares on Chebyshev nodes), and n added to the exponent.  x below kPfPolyLeast becomes
+// it: there n = -127, the polynomial of f = 2^-17 is 33 steps above 1, and its exponent
+// field ends at 0, so the value is 33 2^-149, which is 0 in bf16: a key too far to count
+// adds nothing, however large its V.  Between it and 2^-126 the value is off by up to 2^-127.
 constexpr int kPfPoly = 2;                       // of 8 pairs
 constexpr float kPfPolyLeast = -127.0f + 0x1p-17f;
 __device__ __forceinline__ float2 pf_exp2_poly(float2 x) {

@@ -622,6 +622,7 @@ typedef struct {
  * (t * y_stride), strides >= n_heads * D; y may equal x (same stride: in place)
  * but must not overlap it otherwise.  pos: [n_tok] int32; inv_freq: [rot_dim / 2]
  * f64, radians per position (may be NULL when rot_dim is 0).  n_tok = 0 is a no-op.
+ * n_heads <= 65535, D <= 1024 (else CRS_ERR_UNSUPPORTED).
  * Vectors of up to 16 bytes are used as the sizes, strides and addresses allow. */
 int crs_rope(const crs_rope_params *p, int n_tok, int n_heads, int dtype, const void *x, int64_t x_stride,
              const int32_t *pos, const double *inv_freq, void *y, int64_t y_stride, void *stream);
@@ -642,13 +643,14 @@ int crs_rope(const crs_rope_params *p, int n_tok, int n_heads, int dtype, const 
  *     the next token (it keeps counting when slots are evicted).
  * One step is append (new rows written at slots seq_len .., lengths unchanged),
  * attend (sees them), commit (lengths advance, by fewer than were appended when
- * drafted tokens are rejected); every call but commit can be repeated with the
- * same result.  n_new: [n_seq] int32, the new tokens of each sequence, of which
+ * drafted tokens are rejected).  Append, select, evict, and attend without a mass_out
+ * or with one of its own can be repeated with the same result; attend with mass_out =
+ * mass adds its weights each time, commit its tokens.  n_new: [n_seq] int32, the new tokens of each sequence, of which
  * the first min(max(n_new, 0), n_tok) rows are used; NULL = n_tok for all.
  * Lengths are read on the device, so a captured graph follows them.  A sequence
- * whose new tokens pass cap sets CRS_DEVERR_CAPACITY and the tokens past it are
- * dropped by all three calls.
- * D = 64 or 128, n_seq <= 4096, cap <= max_pages * page_size,
+ * whose new tokens pass cap sets CRS_DEVERR_CAPACITY (in append) and the tokens past it
+ * are dropped by all three calls.
+ * D = 64 or 128, n_seq <= 4096, n_kv <= 4096, cap <= max_pages * page_size,
  * n_pages * page_size < 2^31 (else CRS_ERR_UNSUPPORTED).
  * ====================================================================== */
 typedef struct {
@@ -675,7 +677,8 @@ typedef struct {
  * apart (so that all three may be slices of one projection; q_out is dense).
  * Addresses 16-byte aligned, strides multiples of 8 (else CRS_ERR_INVALID_ARG);
  * the rotated dims are handled in 16-byte pieces: rot_begin a multiple of 8,
- * rot_dim of 16 (else CRS_ERR_UNSUPPORTED). */
+ * rot_dim of 16; 2 n_kv + n_q <= 65535, n_seq * n_tok < 2^31 (else
+ * CRS_ERR_UNSUPPORTED). */
 int crs_cache_append(const crs_cache_params *p, const crs_cache_state *st, const crs_rope_params *r,
                      const double *inv_freq, int n_tok, const int32_t *n_new, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, const void *q, int64_t q_stride, int n_q, void *q_out,
@@ -700,11 +703,16 @@ int crs_cache_commit(const crs_cache_params *p, const crs_cache_state *st, int n
  * mass_out (may be NULL; may be st->mass: in place): for every slot j of
  * sequence s below its length with the new tokens,
  *   mass_out[s, h, j] = decay * mass[s, h, j] + sum over its rows of the weight of j;
- * other slots are left as they were.
+ * other slots are left as they were.  The rows are all that are given, those of drafts that
+ * are rejected later too.  Where only accepted tokens shall count, attend without
+ * mass_out, and once their numbers are known attend again with n_new = accepted and
+ * mass_out, before commit.
  * Arithmetic: products of bf16 values summed in fp32; softmax statistics in fp32;
  * the unnormalised weights enter the second product as bf16 when O is bf16 (one
  * rounding, the size of the output's own) and as three bf16 parts, 24 bits, when
- * O is f32.
+ * O is f32.  They are 2^x by ex2.approx (2^-22); when O is bf16, a quarter of the prefix's,
+ * in batches of more than 16 rows per KV head, are by a polynomial within 2.7e-6, which
+ * lse and the accumulated weights, f32 results, carry too.
  * ====================================================================== */
 typedef struct {
     crs_cache_params c;
@@ -719,8 +727,13 @@ typedef struct {
 
 /* Q: [n_seq, n_tok, n_q, D] bf16; prefix_k, prefix_v: [prefix_len, n_kv, D] bf16
  * (16-byte aligned; may be NULL when prefix_len is 0).  O: [n_seq, n_tok, n_q, D]
- * (16-byte aligned); lse: [n_seq, n_tok, n_q] f32 or NULL.  The workspace size
+ * (16-byte aligned); lse: [n_seq, n_tok, n_q] f32 or NULL.  n_seq * n_tok * n_q < 2^30 and
+ * n_seq * (cap / 64 + 2) < 2^31 (else CRS_ERR_UNSUPPORTED).  The workspace size
  * depends on the current device's SM count: query it with the same device current.
+ * It holds the prefix's partial results, [splits][n_seq * n_tok * n_q][D + 2] f32, where an
+ * f32 O takes a split per 640 prefix keys at least (shorter chains of additions): 109 MB
+ * for 256 sequences of 32 heads of 128 and 16384 keys, against 17 MB for a bf16 O; and,
+ * for mass_out, the slots' logits, [n_seq, n_tok * n_q, cap] f32.
  * Calls that may overlap need workspaces of their own. */
 size_t crs_cache_attn_workspace_size(const crs_cache_attn_params *p);
 int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_state *st, const void *Q, const int32_t *n_new,
@@ -733,8 +746,9 @@ int crs_cache_attn(const crs_cache_attn_params *p, const crs_cache_state *st, co
  * j < seq_len[s] that rank first by (protected first, mass desc, slot asc).  A slot
  * is protected when pos < sink_end or pos >= next_pos[s] - window (pos NULL: none
  * is).  Lists are ascending, -1 padded, as crs_sparse_attn reads them with
- * n_lists = n_kv; count[s] = min(keep, seq_len[s]).  A NaN mass sets
- * CRS_DEVERR_NONFINITE and ranks below every number; seq_len is cut to [0, cap].
+ * n_lists = n_kv; count[s] = min(keep, seq_len[s]).  A NaN mass ranks below every number
+ * and, where slots are dropped (seq_len > keep), sets CRS_DEVERR_NONFINITE; seq_len is
+ * cut to [0, cap].  n_seq * n_kv < 2^31 (else CRS_ERR_UNSUPPORTED).
  * ====================================================================== */
 typedef struct {
     int n_seq, n_kv;
@@ -756,7 +770,8 @@ int crs_mass_select(const crs_mass_select_params *p, const float *mass, const in
  * slots from n on keep their old contents, so the call can be repeated.  idx
  * [n_seq, n_kv, keep] ascending, its first count[s] entries distinct slots of the
  * sequence; count outside [0, min(keep, cap)] is cut to it, an entry outside [0, cap)
- * sets CRS_DEVERR_INDEX and its row is not moved. */
+ * sets CRS_DEVERR_INDEX and its row is not moved.  n_seq * n_kv *
+ * ceil(min(keep, cap / 2) / 128) < 2^31 (else CRS_ERR_UNSUPPORTED). */
 int crs_cache_evict(const crs_cache_params *p, const crs_cache_state *st, int keep, const int32_t *idx,
                     const int32_t *count, void *stream);
 

@@ -338,3 +338,27 @@ def test_far_keys_of_the_prefix_add_nothing(crs, cuda_dev, out_dtype, D, n_seq, 
     c["pk"][column::16] = -12.0
     c["pv"][column::16] = 2.0 ** 126
     check(crs, cuda_dev, c, out_dtype, scale=0.125, with_mass=False)
+
+
+def test_weights_of_accepted_drafts_only(crs, cuda_dev):
+    """Drafts are attended without weights, then once more as far as they were accepted: outputs
+    of the accepted tokens come again, and the weights are those of these tokens alone."""
+    n_tok, lens = 4, [0, 9, 40, 63, 100]
+    c = make(cuda_dev, 5, n_tok, 8, 2, 128, 16, lens, 90, 23)
+    d, cache = on(cuda_dev, c, crs)
+    O, lse = cache.attend(d["q"], d["pk"], d["pv"])
+    assert torch.equal(cache.mass.cpu(), c["mass"])
+    acc = torch.tensor([0, 1, 4, 2, 3], dtype=torch.int32)
+    O2, lse2 = cache.attend(d["q"], d["pk"], d["pv"], n_new=acc.to(cuda_dev), mass_out=cache.mass)
+    _, _, em, A = ref.attend(c["q"], c["k"], c["v"], c["table"], c["seq_len"], c["cap"], acc, c["pk"], c["pv"],
+                             mass=c["mass"])
+    for s in range(5):
+        n, t = int(acc[s]), lens[s] + int(acc[s])
+        # the slots' tiles may be cut elsewhere: twice the f32 tolerance above
+        assert ((O[s, :n] - O2[s, :n]).double().cpu().abs() <= 2 * TOL_F32 * A[s, :n] + 1e-30).all()
+        tol = (em - c["mass"].double()).abs() * 2.0 ** -14 + em.abs() * 2.0 ** -21
+        assert ((cache.mass.double().cpu() - em).abs() <= tol)[s, :, :t].all()
+        assert torch.equal(cache.mass[s, :, t:].cpu(), c["mass"][s, :, t:])
+    cache.commit(acc.to(cuda_dev), n_tok=n_tok)
+    assert cache.seq_len.tolist() == [l + int(a) for l, a in zip(lens, acc)]
+    assert crs.get_device_error() == 0

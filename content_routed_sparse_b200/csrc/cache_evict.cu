@@ -9,9 +9,10 @@
 // registers hold re-read the keys from memory: four passes with 256-bin histograms, then
 // the same placement.
 //
-// Bound: 32 sequences x 4 heads of 30000 to 32768 slots to 4096 take 23 to 29 us; 8 of them are the
-// 34 MB of weights and positions, the rest passes over 32 keys per thread, of which every
-// instruction costs about 0.15 us: one pass counts the bracket, one gathers it, two place.
+// Bound by issue (62%) and the barriers between the passes: 32 sequences x 4 heads of 30000
+// to 32768 slots to 4096 take 23 to 29 us; 8 of them are the 34 MB of weights and positions,
+// the rest passes over 32 keys per thread, of which every instruction costs about 0.15 us:
+// one pass counts the bracket, one gathers it, two place.
 //
 // Eviction: nothing depends on the order of a head's slots, so only the kept slots
 // past the new length move, each into a free slot below it: the r-th of the former

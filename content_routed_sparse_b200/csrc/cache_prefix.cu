@@ -22,7 +22,7 @@
 // Bound: up to 256 rows per KV head by memory (134 MB of K/V for 64 sequences with 4 heads
 // to a group: 41 us, of which 27 are the tiles at 5.5 TB/s), beyond that by the tensor
 // cores: the main loop runs at 1.27 PFLOP/s (256 sequences, 8 heads to a group, 4 KV heads,
-// 16384 keys: 54 us and about 14 us of start and end).  One thread per row instead of two
+// 16384 keys: 54 us and about 13 us of start and end).  One thread per row instead of two
 // ran as fast but held a whole row of S; issuing the products from lane 0 under an
 // ordinary branch cost a fifth (100 us against 79 at the time); O of a tile and S of the
 // next go out together, because the tensor core idles while the issuing thread waits.

@@ -37,6 +37,7 @@ namespace crs {
 constexpr int kPfThreads = 576;
 constexpr int kPfRows = 256;                     // rows of a CTA: two streams of 128
 constexpr uint64_t kPfWaitNs = 1000000000ull;    // 1 s: a wait that long means a fault
+constexpr int kPfSpare = 3 * 1024;               // bytes for the tiles' alignment, PfTop and PfBars
 constexpr float kPfSlack = 8.0f;                 // log2 units a logit may exceed the running shift
 
 template <int D, bool SPLIT> struct PfCfg {
@@ -46,7 +47,7 @@ template <int D, bool SPLIT> struct PfCfg {
     static constexpr int kQ = 128 * D * 2;                   // bytes of a Q tile
     static constexpr int kStages = kTile >= 32768 ? 5 : 8;   // >= 5: see the order of use below
     static constexpr int kTiles = 2 * kQ + kStages * kTile;
-    static constexpr int kSmem = kTiles + 3072;              // the tiles' alignment, PfTop, PfBars
+    static constexpr int kSmem = kTiles + kPfSpare;
     // tensor memory columns: S and the P over it, the parts of P that S cannot hold, O
     static constexpr int kPCols = kKeys / 2;
     static __host__ __device__ constexpr int s_col(int u) { return u * (SPLIT ? 128 : kKeys); }
@@ -66,7 +67,7 @@ typedef float PfTop[2][2][128];                  // [stream][half of a tile's ke
 // All of it is dynamic shared memory: the tiles start `lead` bytes in, on a 1024-byte
 // boundary, PfTop follows them, PfBars take the lead where they fit there, else the end.
 // With a static part the tiles of D = 128 and bf16 output would not fit beside PfTop.
-static_assert(1008 + sizeof(PfTop) <= 3072 && sizeof(PfBars) + sizeof(PfTop) + sizeof(PfBars) <= 3072,
+static_assert(1008 + sizeof(PfTop) <= kPfSpare && sizeof(PfBars) + sizeof(PfTop) + sizeof(PfBars) <= kPfSpare,
               "PfTop always fits behind the tiles, PfBars before them or behind PfTop");
 
 // 2^x of two values on the FMA pipe, for a part of the weights, because the exponential
